@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libmala.so")
 if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"MALA CUDA library not built: {LIB_PATH} is missing "
-        "(run `python -m mass_gated_causal_b200.build` or __graft_entry__.build())")
+        "(run `python mass_gated_causal_b200/build.py` or __graft_entry__.build())")
 
 _lib = ctypes.CDLL(LIB_PATH)
 

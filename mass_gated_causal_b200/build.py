@@ -1,47 +1,82 @@
 """Build the MALA CUDA library (sm_100a) in-tree: mass_gated_causal_b200/libmala.so.
 
-nvcc cross-compiles for sm_100a without a GPU. The library is one translation
-unit (csrc/mala_api.cu includes the kernels) linked with the static CUDA
-runtime, so it carries no dependency on a particular libcudart.
+nvcc cross-compiles for sm_100a without a GPU. Every csrc/*.cu is one
+translation unit, compiled to an object of its own (several at a time, and only
+when one of the files it includes has changed, unless forced) and linked with
+the static CUDA runtime, so the library carries no dependency on a particular
+libcudart. Run as a script (`python mass_gated_causal_b200/build.py`): the
+package itself refuses to import while the library is missing.
 """
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
+OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmala.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-         "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+         "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(os.path.dirname(HERE), "include")]
 
 
 def sources():
-    return sorted(os.path.join(SRC_DIR, f) for f in os.listdir(SRC_DIR) if f.endswith((".cu", ".cuh")))
+    """The library's translation units."""
+    return sorted(os.path.join(SRC_DIR, f) for f in os.listdir(SRC_DIR) if f.endswith(".cu"))
+
+
+def _files_of(src):
+    """A source and every file of this repository that it includes."""
+    seen, todo = set(), [src]
+    while todo:
+        path = os.path.normpath(todo.pop())
+        if path in seen:
+            continue
+        seen.add(path)
+        with open(path) as f:
+            todo += [os.path.join(os.path.dirname(path), x) for x in re.findall(r'^#include "([^"]+)"', f.read(), re.M)]
+    return seen
+
+
+def _object(src):
+    return os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
+
+
+def _stale(out, files) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(f) > os.path.getmtime(out) for f in files)
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    hdr = os.path.join(os.path.dirname(HERE), "include", "mala.h")
-    return any(os.path.getmtime(s) > t for s in sources() + [hdr])
+    return any(_stale(LIB, _files_of(s)) for s in sources())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not needs_build():
         return LIB
+    os.makedirs(OBJ_DIR, exist_ok=True)
+
+    def compile_one(src):
+        obj = _object(src)
+        if force or _stale(obj, _files_of(src)):
+            tmp = obj + f".tmp{os.getpid()}"
+            subprocess.check_call([NVCC] + FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) +
+                                  ["-c", src, "-o", tmp])
+            os.replace(tmp, obj)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=min(len(sources()), os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, sources()))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC] + FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + \
-        [os.path.join(SRC_DIR, "mala_api.cu"), "-o", tmp]
-    subprocess.check_call(cmd)
+    subprocess.check_call([NVCC] + FLAGS + ["-shared"] + objs + ["-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 
 
 if __name__ == "__main__":
-    build(force=True, verbose_ptxas="-v" in sys.argv)
+    build(force="--changed" not in sys.argv, verbose_ptxas="-v" in sys.argv)
     print(LIB)

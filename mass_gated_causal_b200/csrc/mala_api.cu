@@ -1,7 +1,7 @@
 // mala_api.cu -- the C ABI declared in include/mala.h.
 //
 // Host side only: argument validation, TMA tensor-map construction, launch
-// configuration. Every step of the computation runs in the kernels included
+// configuration (what the library's translation units share is in mala_host.h). Every step of the computation runs in the kernels included
 // below. The driver's cuTensorMapEncodeTiled is reached through
 // cudaGetDriverEntryPoint, so the library loads on machines without a GPU
 // driver (its symbols can be inspected there) and needs no -lcuda.
@@ -20,6 +20,11 @@
 #include "mala_decode.cuh"
 #include "mala_decode_exact.cuh"
 #include "mala_fwd.cuh"
+#include "mala_host.h"
+
+using namespace mala::host;
+
+static_assert(kMaxDecodeGroup == mala::kDecMaxG, "one limit for every decode entry point");
 
 namespace {
 
@@ -30,41 +35,24 @@ std::atomic<unsigned long long> g_wait_ns{mala::kWaitLimitNs};
 std::atomic<int> g_stall_tile{-1};
 std::atomic<unsigned long long*> g_v_tiles{nullptr};
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
 
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
+namespace mala {
+namespace host {
+
+unsigned* status_ptr() {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_mala_status) != cudaSuccess) return nullptr;
+  return static_cast<unsigned*>(p);
 }
 
-// Tensor map over a contiguous bf16 BSHD tensor [B, S, H, D] with a
-// {64, 1, rows, 1} box and 128-byte swizzle: one box is a [rows x 64] tile of
-// one head, 128 bytes per row, the layout the UMMA descriptors expect.
-bool make_bshd_map(CUtensorMap* map, const void* base, int B, int S, int H, int D, int rows,
-                   CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(S),
-                        static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H) * D * 2,
-                           static_cast<cuuint64_t>(S) * H * D * 2};
-  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(map, dtype, 4, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+int stall_tile() { return g_stall_tile.load(); }
+
+}  // namespace host
+}  // namespace mala
+
+namespace {
 
 // Tensor map over the fp32 dQ accumulator [B, S, H, D] with a {32, 1, 32, 1}
 // box and 128-byte swizzle: a [32 rows x 32] fp32 block of one head.
@@ -83,15 +71,6 @@ bool make_dq_acc_map(CUtensorMap* map, const void* base, int B, int S, int H, in
   return r == CUDA_SUCCESS;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
-
-unsigned* status_ptr() {
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_mala_status) != cudaSuccess) return nullptr;
-  return static_cast<unsigned*>(p);
-}
-
 int check_train_shape(int B, int Hq, int Hkv, int L, int d, float scale, float tau, int Bq, int Bk) {
   if (B < 1 || Hq < 1 || Hkv < 1 || L < 1) return MALA_ERR_INVALID_ARG;
   if (Hq % Hkv != 0) return MALA_ERR_INVALID_ARG;
@@ -103,23 +82,6 @@ int check_train_shape(int B, int Hq, int Hkv, int L, int d, float scale, float t
   if (static_cast<long long>(B) * L * Hq * d >= (1ll << 40)) return MALA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hq >= (1ll << 24)) return MALA_ERR_UNSUPPORTED;
   return MALA_OK;
-}
-
-template <typename K>
-int set_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
-             ? MALA_OK
-             : MALA_ERR_CUDA;
-}
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-int sm_count() {
-  int sms = 0, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 148;
-  return sms;
 }
 
 // Chunk length of the training kernels' CTA schedule: about one wave of CTAs
@@ -535,21 +497,6 @@ struct Paged {
   const int* block_table = nullptr;
   int max_pages = 0, num_pages = 0;
 };
-
-int check_decode_args(const void* q, const void* kc, const void* vc, const void* o, const float* lse, int B,
-                      int Hq, int Hkv, int Lk, int d, float scale, float tau, int Bk, int n_splits,
-                      const int32_t* kept_tiles) {
-  if (!q || !kc || !vc || !o || !lse || !kept_tiles) return MALA_ERR_INVALID_ARG;
-  if (B < 1 || Hq < 1 || Hkv < 1 || Lk < 1 || Hq % Hkv != 0 || n_splits < 0) return MALA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale) || !(tau >= 0.f) || !std::isfinite(tau)) return MALA_ERR_INVALID_ARG;
-  if ((d != 64 && d != 128) || (Bk != 64 && Bk != 128)) return MALA_ERR_UNSUPPORTED;
-  if (Hq / Hkv > mala::kDecMaxG) return MALA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Lk * Hkv * d >= (1ll << 40)) return MALA_ERR_UNSUPPORTED;
-  const void* ptrs[] = {q, kc, vc, o, lse};
-  for (const void* x : ptrs)
-    if (!aligned16(x)) return MALA_ERR_UNSUPPORTED;
-  return MALA_OK;
-}
 
 // Split kernel + combine into caller-provided partials (parts_base: o partials,
 // then the LSE partials 256 bytes aligned). Lk is the longest sequence's length.
