@@ -385,6 +385,204 @@ MALA_API int mala_decode_noalloc(const void* q, const void* kcache, const void* 
                                  int n_splits, int32_t* kept_tiles, uint8_t* keep_map, void* stream);
 
 /*
+ * mala_rope -- rotary positions with several axes (text, images, video), and
+ * the split of a fused projection's output into contiguous q, k and v.
+ *
+ * The first rotary_dim values of a head form n = rotary_dim / 2 pairs: values
+ * (i, i + n), or (2i, 2i + 1) with MALA_ROPE_ADJACENT. Pair i of token t turns
+ * by theta = positions[axis(i)][t] * inv_freq[i]:
+ *     y1 = x1 cos theta - x2 sin theta,  y2 = x2 cos theta + x1 sin theta
+ * (fp32 arithmetic, the angle reduced in fp64, one rounding to bf16). The other
+ * values of a head, and v, are copied. MALA_ROPE_INVERSE turns by -theta, which
+ * is the gradient (dq, dk, dv of the attention in, the gradient of the
+ * projection's output out).
+ *
+ * axis(i): the pairs are dealt to n_axes axes, sections[a] of them to axis a, in
+ * blocks (the first sections[0] pairs to axis 0, the next to axis 1, ...) or,
+ * with MALA_ROPE_CYCLIC, in turn: pair i belongs to axis a = i mod n_axes if
+ * i < n_axes * sections[a], else to axis 0 (sections that this does not deal
+ * exactly are refused).
+ *
+ *   q, k, v    [T, Hq, d], [T, Hkv, d], [T, Hkv, d] bf16, in, strided; any of
+ *              them may be NULL together with its output
+ *   q_out, k_out, v_out  the same shapes, bf16, out, strided. An output may be
+ *              its own input (the same pointer and strides); apart from that,
+ *              outputs overlap neither inputs nor each other.
+ *   strides    HOST int64 [12], in elements: (token, head) of q, k, v, q_out,
+ *              k_out, v_out. Values of a head are adjacent. Multiples of 8, not
+ *              negative; of the outputs at least d.
+ *   positions  [n_axes, T] int32, in (any value, negative too)
+ *   inv_freq   [rotary_dim / 2] fp32, in
+ *   T >= 0 (0: nothing is done); d in {64, 128}; rotary_dim a multiple of 16,
+ *   16 <= rotary_dim <= d; 1 <= n_axes <= 4; sections: HOST int32 [n_axes],
+ *   not negative, their sum rotary_dim / 2
+ */
+#define MALA_ROPE_ADJACENT 1u
+#define MALA_ROPE_CYCLIC 2u
+#define MALA_ROPE_INVERSE 4u
+MALA_API int mala_rope(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
+             const int64_t* strides, const int32_t* positions, const float* inv_freq, int T, int Hq, int Hkv, int d,
+             int rotary_dim, const int32_t* sections, int n_axes, unsigned flags, void* stream);
+
+/*
+ * mala_rope_append -- mala_rope of the new tokens of a serving step, their keys
+ * and values written straight into a paged cache (the layout mala_decode_paged
+ * reads).
+ *
+ * The new tokens of sequence s are rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of
+ * q, k and v, or, with cu_seqlens NULL, n = T / num_seqs tokens each in order
+ * (n = 1: one decoding step). They are the last tokens of the sequence:
+ * seqlens_k[s] is its length with them, and its i-th of n_s new tokens goes to
+ * cache row seqlens_k[s] - n_s + i. positions are the tokens' rotary positions,
+ * which need not be their rows (several axes; a cache that lost rows).
+ *
+ *   q, q_out   may both be NULL; strides HOST int64 [8]: (token, head) of q, k,
+ *              v, q_out, as for mala_rope
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, d] bf16, out: only the new
+ *              tokens' rows are written
+ *   block_table [num_seqs, max_pages_per_seq], seqlens_k [num_seqs], cu_seqlens
+ *              [num_seqs + 1] int32, DEVICE memory
+ *   other arguments as for mala_rope (MALA_ROPE_INVERSE is refused)
+ * A sequence of length 0 is an idle slot: its tokens are left alone, q_out rows
+ * included, and so are tokens that no sequence owns. A length below the new
+ * tokens or above max_pages_per_seq * page_size, or a page id outside
+ * [0, num_pages), is reported by mala_check_status as MALA_ERR_INVALID_ARG (the
+ * token's q is rotated, its k and v are not written). Two tokens must not share
+ * a cache row.
+ */
+MALA_API int mala_rope_append(const void* q, const void* k, const void* v, void* q_out, const int64_t* strides,
+             const int32_t* positions, const float* inv_freq, void* k_pages, void* v_pages,
+             const int32_t* block_table, const int32_t* seqlens_k, const int32_t* cu_seqlens, int num_seqs, int T,
+             int Hq, int Hkv, int num_pages, int page_size, int max_pages_per_seq, int d, int rotary_dim,
+             const int32_t* sections, int n_axes, unsigned flags, void* stream);
+
+/*
+ * Workspace bytes mala_key_mass needs (0: none, and 0 for invalid sizes): the
+ * partial sums of walks that are cut into chunks because the keys alone do not
+ * fill the GPU. Depends on its arguments and the current device's SM count.
+ */
+MALA_API size_t mala_key_mass_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk, int window);
+MALA_API size_t mala_key_mass_varlen_workspace_size(int num_seqs, int Hq, int Hkv, int max_seqlen_q,
+             int max_seqlen_k, int total_q, int window);
+
+/*
+ * mala_key_mass -- the attention weight ("mass") each key of a prompt has
+ * collected, from the q, k and LSE of a mala_fwd or mala_prefill call.
+ *
+ *     mass_out[b, hkv, j] = decay * mass_in[b, hkv, j]
+ *         + sum over rows i that see key j and heads h of the group of exp(s_ij - LSE_i)
+ *
+ * The Lq queries are the last Lq of the Lk positions, as in mala_prefill. Rows
+ * that count: the last `window` of the Lq (0, or at least Lq: all). Keys j >=
+ * Lk - Lq are the queries' own tokens and start from 0 (mass_in is not read
+ * there). The weights are those of every visible key, whatever tiles a gate
+ * (tau > 0) skipped; with tau = 0 each row's weights sum to 1. The sums are
+ * fp32, in an order that does not depend on the schedule.
+ *
+ *   q [B, Lq, Hq, d], k [B, Lk, Hkv, d] bf16, lse [B, Hq, Lq] fp32, in (finite;
+ *              a row whose LSE is +infinity adds nothing)
+ *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
+ *   mass_out   [B, Hkv, ld_mass] fp32, out; entries j >= Lk become 0. May be
+ *              mass_in.
+ *   ld_mass >= Lk, decay >= 0, window >= 0; workspace 256-byte aligned, >=
+ *   mala_key_mass_workspace_size(...) bytes (NULL if that is 0)
+ */
+MALA_API int mala_key_mass(const void* q, const void* k, const float* lse, const float* mass_in, float* mass_out,
+             int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale, int window, float decay, int ld_mass,
+             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mala_key_mass_varlen -- mala_key_mass of a packed batch (the q, k, LSE and
+ * tables of a mala_fwd_varlen call); sequence s fills row s of the masses.
+ *
+ *   mass_in, mass_out [num_seqs, Hkv, ld_mass] fp32, ld_mass >= max_seqlen_k
+ *   (entries past a sequence's keys become 0)
+ * A sequence whose table entries are invalid (as in mala_fwd_varlen) is left
+ * untouched and reported by mala_check_status.
+ */
+MALA_API int mala_key_mass_varlen(const void* q, const void* k, const float* lse, const int32_t* cu_seqlens_q,
+             const int32_t* cu_seqlens_k, const float* mass_in, float* mass_out, int num_seqs, int max_seqlen_q,
+             int max_seqlen_k, int total_q, int total_k, int Hq, int Hkv, int d, float scale, int window, float decay,
+             int ld_mass, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes mala_decode_paged_mass needs: fp32 scores [B, Hkv,
+ * max_pages_per_seq * page_size, Hq / Hkv] and the split partials of
+ * mala_decode_workspace_size, each 256-byte aligned. 0 for invalid sizes.
+ */
+MALA_API size_t mala_decode_mass_workspace_size(int B, int Hq, int d, int page_size, int max_pages_per_seq,
+             int n_splits);
+
+/*
+ * mala_decode_paged_mass -- mala_decode_paged that also collects each key's
+ * attention weight (every tile is scored anyway, kept or skipped):
+ *
+ *     mass_out[b, hkv, j] = decay * mass_in[b, hkv, j] + sum over heads h of the group of exp(s_hj - LSE_h)
+ *
+ * O, LSE, kept_tiles and keep_map are those of mala_decode_paged. The newest key
+ * (j = seqlens_k[b] - 1) is the query's own and starts from 0. A sequence of
+ * length 0 is an idle slot: O = 0, LSE = -infinity, masses 0, no error.
+ *
+ *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
+ *   mass_out   [B, Hkv, ld_mass] fp32, out; entries past a sequence's keys
+ *              become 0. May be mass_in.
+ *   ld_mass >= max_pages_per_seq * page_size; decay >= 0
+ *   workspace  >= mala_decode_mass_workspace_size(...) bytes, 256-byte aligned
+ */
+MALA_API int mala_decode_paged_mass(const void* q, const void* k_pages, const void* v_pages,
+             const int32_t* block_table, const int32_t* seqlens_k, void* o, float* lse, const float* mass_in,
+             float* mass_out, int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages_per_seq, int d,
+             float scale, float tau, float decay, int ld_mass, int n_splits, void* workspace, size_t workspace_bytes,
+             int32_t* kept_tiles, uint8_t* keep_map, void* stream);
+
+/*
+ * mala_evict_select -- which rows of each cache remain when it is cut down to
+ * `budget` rows, by collected attention weight.
+ *
+ * Sequence b has L = seqlens_k[b] rows. If L <= budget all remain. Else, for each
+ * KV head, the first n_sink and the last n_recent rows remain, and of the rows
+ * between them the budget - n_sink - n_recent of largest mass; equal masses are
+ * taken from the lowest row up, and NaN ranks with -infinity. Rows keep their
+ * order.
+ *
+ *   mass       [B, Hkv, ld_mass] fp32, in
+ *   seqlens_k  [B] int32, DEVICE memory, in (0 <= length <= ld_mass; another
+ *              length is reported by mala_check_status and counts as 0)
+ *   index      [B, Hkv, budget] int32, out: the remaining rows, ascending; -1
+ *              past min(L, budget)
+ *   new_seqlens [B] int32, out: min(L, budget) (not the array seqlens_k)
+ *   mass_out   [B, Hkv, ld_mass_out] fp32, out, nullable: the remaining rows'
+ *              masses, 0 past them; ld_mass_out >= budget
+ *   budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget
+ */
+MALA_API int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* index, int32_t* new_seqlens,
+             float* mass_out, int B, int Hkv, int ld_mass, int budget, int n_sink, int n_recent, int ld_mass_out,
+             void* stream);
+
+/*
+ * mala_evict_gather -- copies the remaining rows' K and V into other pages: row
+ * index[b, hkv, r] of sequence b's cache becomes row r of the cache that
+ * out_table[b] describes, for r < new_seqlens[b] and every KV head. Pages may be
+ * shared by several sequences of block_table (a common prefix); nothing of the
+ * old cache is changed.
+ *
+ *   k_pages, v_pages [num_pages, page_size, Hkv, d] bf16, in; k_out_pages,
+ *              v_out_pages [num_out_pages, page_size, Hkv, d] bf16, out. They may
+ *              be the same pools; the pages of out_table are then not among
+ *              those of block_table, and in any case named once.
+ *   block_table [B, max_pages_per_seq], out_table [B, max_out_pages_per_seq],
+ *              index, new_seqlens (as mala_evict_select writes them) int32,
+ *              DEVICE memory; max_out_pages_per_seq * page_size >= budget
+ * Rows past new_seqlens[b] are left as they were. A page id or an index out of
+ * range is reported by mala_check_status as MALA_ERR_INVALID_ARG (that row is
+ * not copied).
+ */
+MALA_API int mala_evict_gather(const void* k_pages, const void* v_pages, const int32_t* block_table,
+             const int32_t* index, const int32_t* new_seqlens, void* k_out_pages, void* v_out_pages,
+             const int32_t* out_table, int B, int Hkv, int budget, int num_pages, int num_out_pages, int page_size,
+             int max_pages_per_seq, int max_out_pages_per_seq, int d, void* stream);
+
+/*
  * mala_test_hooks -- switches for tests of the failure path and of the V
  * traffic. Process-wide; they apply to calls enqueued after this one (on any
  * stream) until changed, and are not meant for production use. The pages
@@ -395,9 +593,11 @@ MALA_API int mala_decode_noalloc(const void* q, const void* kcache, const void* 
  *   stall_tile     -1: off. >= 0: the MMA issuer of mala_fwd / mala_prefill /
  *                  mala_fwd_varlen / mala_bwd / mala_bwd_varlen, and the K
  *                  producer of mala_decode / mala_decode_paged /
- *                  mala_decode_noalloc, wait before key tile `stall_tile` on a
- *                  barrier nothing completes, so that the wait expires: the
- *                  kernel then leaves through its abort path and
+ *                  mala_decode_paged_mass / mala_decode_noalloc, wait before key
+ *                  tile `stall_tile` (the MMA issuer of mala_key_mass /
+ *                  mala_key_mass_varlen: before its walk's item `stall_tile`)
+ *                  on a barrier nothing completes, so that the wait expires:
+ *                  the kernel then leaves through its abort path and
  *                  mala_check_status returns MALA_ERR_DEVICE_TIMEOUT. Outputs
  *                  of such a call are undefined.
  *   fwd_v_tiles    NULL: off. Else a DEVICE uint64 the forward kernels (gate

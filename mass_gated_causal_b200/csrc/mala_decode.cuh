@@ -35,6 +35,9 @@
 //
 // mala_decode_combine_kernel: LSE = log sum_s exp(LSE_s),
 // O = sum_s exp(LSE_s - LSE) O_s, one warp per (b, query head).
+//
+// A decode that also collects each key's attention weight (kScores) keeps the
+// scores it computes anyway; mala_decode_mass.cuh turns them into weights.
 #pragma once
 
 #include "mala_ptx.cuh"
@@ -62,6 +65,7 @@ struct DecParams {
   unsigned* status;
   uint64_t wait_ns;  // limit of each bounded wait
   int stall_tile;    // test hook (-1: off): the K producer stalls before this tile
+  float* scores;     // kScores: [B, Hkv, max_pages * Bk, G] scores in log2 units (live keys only)
 };
 
 // Sum N per-lane values over the L lanes of a group (lane index c = lane % L,
@@ -146,8 +150,10 @@ struct DecLayout {
 };
 
 // kPaged: a paged cache (p.seqlens and p.block_table set); the contiguous
-// instantiation keeps every length a kernel parameter.
-template <int D, int BK, int GP, bool kGate, bool kPaged>
+// instantiation keeps every length a kernel parameter. kScores (paged only):
+// every live key's score is written to p.scores, and a sequence of length 0 is
+// an idle slot (O = 0, LSE = -infinity) instead of an invalid length.
+template <int D, int BK, int GP, bool kGate, bool kPaged, bool kScores = false>
 __global__ void __launch_bounds__(320, 1)
     mala_decode_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                              const DecParams p) {
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(320, 1)
     atomicOr(p.status, kStatusSeqTable);
     return p.num_pages;
   };
-  if (bad && sp_idx == 0 && tid == 0) atomicOr(p.status, kStatusSeqTable);
+  if (bad && sp_idx == 0 && tid == 0 && !(kScores && __ldg(p.seqlens + b) == 0)) atomicOr(p.status, kStatusSeqTable);
 
   if (T <= 0) {  // empty split: contributes nothing to the merge
     for (int i = tid; i < G * D; i += blockDim.x) {
@@ -386,6 +392,12 @@ __global__ void __launch_bounds__(320, 1)
 
   auto row_addr = [&](uint32_t base, int j) { return base + chunk_atom + j * 128 + ((chunk_in ^ (j & 7)) << 4); };
 
+  // kScores: this (b, KV head)'s scores, G to a key
+  float* score_row = kScores ? p.scores + static_cast<size_t>(b * p.Hkv + hkv) * p.max_pages * BK * G : nullptr;
+  // paged: rows of the split's newest tile (always its first kept one) that hold keys. The rest
+  // of its page is whatever the pool held, perhaps not finite, and 0 times that is not 0.
+  const int live0 = kPaged ? Lk - (t1 - 1) * BK : BK;
+
   float sc_cur[NR], sc_nxt[NR];  // scores (batched: my step's key, heads g0 ..; else head hh, every step)
   auto score = [&](int t, float (&sc)[NR]) {
     const int st = t % NK;
@@ -421,6 +433,7 @@ __global__ void __launch_bounds__(320, 1)
       for (int i = 0; i < VPL; ++i) {
         sc[i] = live ? part[i] : -INFINITY;
         mx[i] = sc[i];
+        if (kScores && live && g0 + i < G) score_row[static_cast<size_t>(kb * BK + j) * G + g0 + i] = part[i] * c2;
       }
       // max over the warp's keys: the other steps' lanes, then the other key groups
 #pragma unroll
@@ -458,6 +471,8 @@ __global__ void __launch_bounds__(320, 1)
         const bool live = kb * BK + j < Lk;
         if (live) mx = fmaxf(mx, mine);
         sc[s2] = live ? mine : -INFINITY;
+        if (kScores && live && hh < G && (c % LPH) == 0)
+          score_row[static_cast<size_t>(kb * BK + j) * G + hh] = mine * c2;
       }
       mbar_arrive(&k_empty[st]);  // my reads of this K stage are done
 #pragma unroll
@@ -472,6 +487,7 @@ __global__ void __launch_bounds__(320, 1)
     const int vs = n % NV, ps = n % NP;
     const bool okv = mbar_wait_warp(&v_full[vs], (n / NV) & 1, fs);
     if (!okv) { aborted = true; return; }
+    const int live_v = n == 0 ? live0 : BK;
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
       const float al = sAlpha[ps * GP + g];
@@ -482,8 +498,8 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
     for (int s2 = 0; s2 < STEPS; ++s2) {
       const int j = warp * KPWT + s2 * KPW + kg;
-      uint32_t a[4];
-      ld_shared_v4(row_addr(sVa + vs * TB, j), a[0], a[1], a[2], a[3]);
+      uint32_t a[4] = {0u, 0u, 0u, 0u};
+      if (!kPaged || j < live_v) ld_shared_v4(row_addr(sVa + vs * TB, j), a[0], a[1], a[2], a[3]);
       uint64_t vf[4];
 #pragma unroll
       for (int e2 = 0; e2 < 4; ++e2) vf[e2] = bf16x2_to_f2(a[e2]);

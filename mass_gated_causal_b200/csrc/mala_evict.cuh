@@ -1,0 +1,270 @@
+// mala_evict.cuh -- eviction from a paged cache by collected attention weight.
+//
+// mala_evict_select_kernel: which rows of a sequence's cache remain, for every
+// (sequence, KV head). With L rows and a budget of K < L, the first n_sink and
+// the last n_recent rows remain, and of the rows between them the
+// need = K - n_sink - n_recent heaviest, ties to the lowest row. The kernel
+// finds the need-th largest mass by a radix select over the masses' ordered bit
+// patterns (11, 11 and 10 bits, most significant first), then lists the rows
+// above it and the first of those equal to it in ascending order. One cluster of
+// kCluster CTAs works on one row of masses, each CTA on a contiguous part: the
+// digit counts are joined through distributed shared memory, and the parts'
+// output offsets are the counts of the CTAs before them, so nothing depends on
+// the order of atomics. The masses are read five times, from L2 after the first.
+//
+// mala_evict_gather_kernel: copies the K and V of the remaining rows into other
+// pages. Bound by HBM: each kept row of a head is read and written once, in
+// pieces of D * 2 bytes on the reading side (rows of the other heads lie
+// between) and whole lines on the writing side.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "mala_ptx.cuh"
+
+namespace mala {
+
+struct EvictParams {
+  const float* mass;  // [B, Hkv, ld]
+  const int32_t* seqlens;
+  int32_t* index;     // [B, Hkv, budget]
+  int32_t* new_lens;  // [B]
+  float* mass_out;    // [B, Hkv, ld_out], nullable
+  int B, Hkv, ld, budget, n_sink, n_recent, ld_out;
+  unsigned* status;
+};
+
+constexpr int kEvictThreads = 512;
+constexpr int kEvictBins = 2048;
+
+// Bit pattern whose unsigned order is the masses' order: -0 equals +0, and NaN
+// ranks with -infinity.
+__device__ __forceinline__ uint32_t mass_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  if (x != x) return 0x007fffffu;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+template <int kCluster>
+__global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const EvictParams p) {
+  namespace cg = cooperative_groups;
+  constexpr int NT = kEvictThreads, NW = NT / 32, BPT = kEvictBins / NT;
+  __shared__ uint32_t hist[kEvictBins];
+  __shared__ uint32_t wsum[NW];
+  __shared__ uint32_t s_digit, s_above;
+  __shared__ uint32_t w_gt[NW], w_eq[NW];
+  __shared__ uint32_t cta_cnt[2];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  const int b = row / p.Hkv, h = row % p.Hkv;
+  int L = __ldg(p.seqlens + b);
+  if (L < 0 || L > p.ld) {  // an invalid length is reported, and nothing of the sequence remains
+    if (h == 0 && rank == 0 && tid == 0) atomicOr(p.status, kStatusSeqTable);
+    L = 0;
+  }
+  const int n_new = min(L, p.budget);
+  const float* mass = p.mass + static_cast<size_t>(row) * p.ld;
+  int32_t* index = p.index + static_cast<size_t>(row) * p.budget;
+  float* mass_out = p.mass_out ? p.mass_out + static_cast<size_t>(row) * p.ld_out : nullptr;
+  const int gt = rank * NT + tid, gn = kCluster * NT;
+  if (h == 0 && gt == 0) p.new_lens[b] = n_new;
+  for (int r = n_new + gt; r < p.budget; r += gn) index[r] = -1;
+  if (mass_out)
+    for (int r = n_new + gt; r < p.ld_out; r += gn) mass_out[r] = 0.f;
+  if (L <= p.budget) {  // everything remains (the same for every CTA of the cluster)
+    for (int r = gt; r < L; r += gn) {
+      index[r] = r;
+      if (mass_out) mass_out[r] = mass[r];
+    }
+    return;
+  }
+
+  const int lo = p.n_sink, hi = L - p.n_recent;  // L > budget >= n_sink + n_recent
+  const int need = p.budget - p.n_sink - p.n_recent;
+  for (int r = gt; r < lo; r += gn) {
+    index[r] = r;
+    if (mass_out) mass_out[r] = mass[r];
+  }
+  for (int r = hi + gt; r < L; r += gn) {
+    const int at = p.budget - (L - r);
+    index[at] = r;
+    if (mass_out) mass_out[at] = mass[r];
+  }
+  if (need == 0) return;  // uniform over the cluster
+
+  cg::cluster_group cluster = cg::this_cluster();
+  // this CTA's part of the rows between, in whole runs of 32 rows per warp
+  const int mid = hi - lo;
+  const int per_warp = ((mid + kCluster * NW - 1) / (kCluster * NW) + 31) & ~31;
+  const int c0 = lo + min(rank * NW * per_warp, mid), c1 = lo + min((rank + 1) * NW * per_warp, mid);
+
+  uint32_t prefix = 0, mask = 0;
+  uint32_t remaining = static_cast<uint32_t>(need);
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bins = pass == 2 ? 1024u : 2048u;
+    for (int i = tid; i < kEvictBins; i += NT) hist[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int r = c0 + tid; r < c1; r += NT) {
+      const uint32_t key = mass_key(mass[r]);
+      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+    }
+    cluster.sync();
+    // counts of this thread's bins over the cluster; thread 0 takes the highest
+    uint32_t cnt[BPT], sum = 0;
+#pragma unroll
+    for (int i = 0; i < BPT; ++i) cnt[i] = 0;
+    const int top = kEvictBins - 1 - tid * BPT;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      const uint32_t* other = kCluster == 1 ? hist : cluster.map_shared_rank(hist, c);
+#pragma unroll
+      for (int i = 0; i < BPT; ++i) cnt[i] += other[top - i];
+    }
+#pragma unroll
+    for (int i = 0; i < BPT; ++i) sum += cnt[i];
+    uint32_t incl = sum;  // inclusive scan over the threads, from the highest bin down
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (before < remaining && before + sum >= remaining) {  // one thread: the digit is among its bins
+      uint32_t above = before;
+      int digit = top;
+#pragma unroll
+      for (int i = 0; i < BPT; ++i) {
+        if (above + cnt[i] >= remaining) {
+          digit = top - i;
+          break;
+        }
+        above += cnt[i];
+      }
+      s_digit = static_cast<uint32_t>(digit);
+      s_above = above;
+    }
+    __syncthreads();
+    remaining -= s_above;
+    prefix |= s_digit << shift;
+    mask |= (bins - 1) << shift;
+    cluster.sync();  // every CTA has read this pass's counts
+  }
+
+  // rows above the threshold, and the first `remaining` of those equal to it
+  const int w0 = min(c0 + warp * per_warp, c1), w1 = min(w0 + per_warp, c1);
+  uint32_t n_gt = 0, n_eq = 0;
+#pragma unroll 4
+  for (int r = w0 + lane; r < w1; r += 32) {
+    const uint32_t key = mass_key(mass[r]);
+    n_gt += key > prefix ? 1u : 0u;
+    n_eq += key == prefix ? 1u : 0u;
+  }
+  n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+  n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+  if (lane == 0) {
+    w_gt[warp] = n_gt;
+    w_eq[warp] = n_eq;
+  }
+  __syncthreads();
+  if (tid < 2) {
+    uint32_t s = 0;
+    for (int w = 0; w < NW; ++w) s += tid == 0 ? w_gt[w] : w_eq[w];
+    cta_cnt[tid] = s;
+  }
+  cluster.sync();
+  uint32_t base_gt = 0, base_eq = 0;
+  for (int c = 0; c < rank; ++c) {
+    const uint32_t* other = cluster.map_shared_rank(cta_cnt, c);
+    base_gt += other[0];
+    base_eq += other[1];
+  }
+  for (int w = 0; w < warp; ++w) {
+    base_gt += w_gt[w];
+    base_eq += w_eq[w];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int r0 = w0; r0 < w1; r0 += 32) {
+    const int r = r0 + lane;
+    const float m = r < w1 ? mass[r] : 0.f;
+    const uint32_t key = mass_key(m);
+    const bool is_gt = r < w1 && key > prefix, is_eq = r < w1 && key == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+    const uint32_t eq_rank = base_eq + __popc(be & below);
+    if (is_gt || (is_eq && eq_rank < remaining)) {
+      const int at = lo + static_cast<int>(base_gt + __popc(bg & below) + min(eq_rank, remaining));
+      index[at] = r;
+      if (mass_out) mass_out[at] = m;
+    }
+    base_gt += __popc(bg);
+    base_eq += __popc(be);
+  }
+  cluster.sync();  // no CTA leaves while another may read its counts
+}
+
+struct GatherParams {
+  const uint4* k;  // [num_pages, page, Hkv, d]
+  const uint4* v;
+  uint4* k_out;    // [num_out_pages, page, Hkv, d]
+  uint4* v_out;
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* out_table;    // [B, max_out_pages]
+  const int32_t* index;        // [B, Hkv, budget]
+  const int32_t* lens;         // [B] rows that remain
+  int B, Hkv, budget, num_pages, max_pages, num_out_pages, max_out_pages, page_shift;
+  unsigned* status;
+};
+
+constexpr int kGatherThreads = 256;
+constexpr int kGatherRows = 4;  // rows of a head a thread copies 16 bytes of, K and V
+
+template <int D>
+__global__ void __launch_bounds__(kGatherThreads) mala_evict_gather_kernel(const GatherParams p) {
+  constexpr int LPR = D / 8, SLOTS = kGatherThreads / LPR;
+  const int b = blockIdx.y;
+  const int len = min(__ldg(p.lens + b), p.budget);
+  const int c = threadIdx.x % LPR;
+  const long long n = static_cast<long long>(max(len, 0)) * p.Hkv;  // (row, head) pairs, heads fastest
+  const long long first = static_cast<long long>(blockIdx.x) * SLOTS * kGatherRows + threadIdx.x / LPR;
+  const int page_mask = (1 << p.page_shift) - 1;
+  long long src[kGatherRows], dst[kGatherRows];
+  uint4 kv[kGatherRows], vv[kGatherRows];
+#pragma unroll
+  for (int u = 0; u < kGatherRows; ++u) {
+    const long long i = first + u * SLOTS;
+    src[u] = -1;
+    if (i >= n) continue;
+    const int r = static_cast<int>(i / p.Hkv), h = static_cast<int>(i % p.Hkv);
+    const int from = __ldg(p.index + (static_cast<long long>(b) * p.Hkv + h) * p.budget + r);
+    const int to_pg = __ldg(p.out_table + static_cast<long long>(b) * p.max_out_pages + (r >> p.page_shift));
+    int pg = -1;
+    if (from >= 0 && (from >> p.page_shift) < p.max_pages)
+      pg = __ldg(p.block_table + static_cast<long long>(b) * p.max_pages + (from >> p.page_shift));
+    if (pg < 0 || pg >= p.num_pages || to_pg < 0 || to_pg >= p.num_out_pages) {
+      if (c == 0) atomicOr(p.status, kStatusSeqTable);
+      continue;
+    }
+    src[u] = (((static_cast<long long>(pg) << p.page_shift) + (from & page_mask)) * p.Hkv + h) * LPR + c;
+    dst[u] = (((static_cast<long long>(to_pg) << p.page_shift) + (r & page_mask)) * p.Hkv + h) * LPR + c;
+  }
+#pragma unroll
+  for (int u = 0; u < kGatherRows; ++u)
+    if (src[u] >= 0) {
+      kv[u] = p.k[src[u]];
+      vv[u] = p.v[src[u]];
+    }
+#pragma unroll
+  for (int u = 0; u < kGatherRows; ++u)
+    if (src[u] >= 0) {
+      p.k_out[dst[u]] = kv[u];
+      p.v_out[dst[u]] = vv[u];
+    }
+}
+
+}  // namespace mala

@@ -104,17 +104,6 @@ struct FwdLayout {
   static_assert(ALLOC_BYTES <= 232448, "forward shared memory exceeds the per-CTA limit");
 };
 
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16 (A in tensor memory).
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // kMode: 0 = no gate (tau = 0: every legal tile kept, V fetched ahead);
 // 1 = gate, V requested only for tiles a query block keeps (the default);
 // 2 = gate, V of every tile fetched ahead whatever the vote (opt-in: skipped
