@@ -229,10 +229,17 @@ int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* inde
   p.status = status_ptr();
   if (!p.status) return MALA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // CTAs per row of masses: enough for about 4K masses a CTA
-  if (ld_mass <= 4096) return launch_select<1>(p, st);
-  if (ld_mass <= 16384) return launch_select<4>(p, st);
-  return launch_select<8>(p, st);
+  // CTAs per row of masses: as many as keep all rows on the GPU at once, but
+  // no more than leave each 2K masses
+  const long long rows = static_cast<long long>(B) * Hkv;
+  int cluster = 1;
+  while (cluster < 8 && rows * cluster * 2 <= sm_count() && ld_mass > 2048 * cluster) cluster *= 2;
+  switch (cluster) {
+    case 1: return launch_select<1>(p, st);
+    case 2: return launch_select<2>(p, st);
+    case 4: return launch_select<4>(p, st);
+    default: return launch_select<8>(p, st);
+  }
 }
 
 int mala_evict_gather(const void* k_pages, const void* v_pages, const int32_t* block_table, const int32_t* index,

@@ -34,7 +34,7 @@ struct EvictParams {
   unsigned* status;
 };
 
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 1024;
 constexpr int kEvictBins = 2048;
 
 // Bit pattern whose unsigned order is the masses' order: -0 equals +0, and NaN
@@ -45,14 +45,21 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Sum over the warps before this one (wsum: a value per warp, in shared memory).
+template <int NW>
+__device__ __forceinline__ uint32_t before_warp(const uint32_t* wsum, int warp, int lane) {
+  static_assert(NW == 32, "one value per lane");
+  return __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
+}
+
 template <int kCluster>
 __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const EvictParams p) {
   namespace cg = cooperative_groups;
-  constexpr int NT = kEvictThreads, NW = NT / 32, BPT = kEvictBins / NT;
-  __shared__ uint32_t hist[kEvictBins];
-  __shared__ uint32_t wsum[NW];
+  constexpr int NT = kEvictThreads, NW = NT / 32;
+  static_assert(kEvictBins == 2 * NT, "two bins per thread");
+  __shared__ __align__(16) uint32_t hist[3][kEvictBins];  // one per pass: no pass waits for the last one's readers
+  __shared__ uint32_t wsum[NW], w_gt[NW], w_eq[NW];
   __shared__ uint32_t s_digit, s_above;
-  __shared__ uint32_t w_gt[NW], w_eq[NW];
   __shared__ uint32_t cta_cnt[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,73 +101,66 @@ __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const 
   if (need == 0) return;  // uniform over the cluster
 
   cg::cluster_group cluster = cg::this_cluster();
+  auto sync_all = [&]() {
+    if constexpr (kCluster == 1) __syncthreads();
+    else cluster.sync();
+  };
   // this CTA's part of the rows between, in whole runs of 32 rows per warp
   const int mid = hi - lo;
   const int per_warp = ((mid + kCluster * NW - 1) / (kCluster * NW) + 31) & ~31;
   const int c0 = lo + min(rank * NW * per_warp, mid), c1 = lo + min((rank + 1) * NW * per_warp, mid);
 
+#pragma unroll
+  for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(&hist[i][2 * tid]) = make_uint2(0u, 0u);
+  __syncthreads();
   uint32_t prefix = 0, mask = 0;
   uint32_t remaining = static_cast<uint32_t>(need);
-#pragma unroll 1
+#pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    constexpr int kShift[3] = {21, 10, 0};
+    const int shift = kShift[pass];
     const uint32_t bins = pass == 2 ? 1024u : 2048u;
-    for (int i = tid; i < kEvictBins; i += NT) hist[i] = 0;
-    __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
     for (int r = c0 + tid; r < c1; r += NT) {
       const uint32_t key = mass_key(mass[r]);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+      if ((key & mask) == prefix) atomicAdd(&hist[pass][(key >> shift) & (bins - 1)], 1u);
     }
-    cluster.sync();
-    // counts of this thread's bins over the cluster; thread 0 takes the highest
-    uint32_t cnt[BPT], sum = 0;
-#pragma unroll
-    for (int i = 0; i < BPT; ++i) cnt[i] = 0;
-    const int top = kEvictBins - 1 - tid * BPT;
+    sync_all();
+    // counts of this thread's two bins over the cluster; thread 0 takes the highest
+    const int top = kEvictBins - 2 - 2 * tid;
+    uint2 cnt = make_uint2(0u, 0u);
 #pragma unroll
     for (int c = 0; c < kCluster; ++c) {
-      const uint32_t* other = kCluster == 1 ? hist : cluster.map_shared_rank(hist, c);
-#pragma unroll
-      for (int i = 0; i < BPT; ++i) cnt[i] += other[top - i];
+      const uint32_t* other = kCluster == 1 ? hist[pass] : cluster.map_shared_rank(&hist[pass][0], c);
+      const uint2 v = *reinterpret_cast<const uint2*>(other + top);
+      cnt.x += v.x;
+      cnt.y += v.y;
     }
-#pragma unroll
-    for (int i = 0; i < BPT; ++i) sum += cnt[i];
+    const uint32_t sum = cnt.x + cnt.y;
     uint32_t incl = sum;  // inclusive scan over the threads, from the highest bin down
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    uint32_t before = incl - sum;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (before < remaining && before + sum >= remaining) {  // one thread: the digit is among its bins
-      uint32_t above = before;
-      int digit = top;
-#pragma unroll
-      for (int i = 0; i < BPT; ++i) {
-        if (above + cnt[i] >= remaining) {
-          digit = top - i;
-          break;
-        }
-        above += cnt[i];
-      }
-      s_digit = static_cast<uint32_t>(digit);
-      s_above = above;
+    const uint32_t above = before_warp<NW>(wsum, warp, lane) + incl - sum;
+    if (above < remaining && above + sum >= remaining) {  // one thread: the digit is one of its bins
+      const bool high = above + cnt.y >= remaining;
+      s_digit = static_cast<uint32_t>(high ? top + 1 : top);
+      s_above = high ? above : above + cnt.y;
     }
     __syncthreads();
     remaining -= s_above;
     prefix |= s_digit << shift;
     mask |= (bins - 1) << shift;
-    cluster.sync();  // every CTA has read this pass's counts
   }
 
   // rows above the threshold, and the first `remaining` of those equal to it
   const int w0 = min(c0 + warp * per_warp, c1), w1 = min(w0 + per_warp, c1);
   uint32_t n_gt = 0, n_eq = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int r = w0 + lane; r < w1; r += 32) {
     const uint32_t key = mass_key(mass[r]);
     n_gt += key > prefix ? 1u : 0u;
@@ -173,23 +173,22 @@ __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const 
     w_eq[warp] = n_eq;
   }
   __syncthreads();
-  if (tid < 2) {
-    uint32_t s = 0;
-    for (int w = 0; w < NW; ++w) s += tid == 0 ? w_gt[w] : w_eq[w];
-    cta_cnt[tid] = s;
-  }
-  cluster.sync();
-  uint32_t base_gt = 0, base_eq = 0;
-  for (int c = 0; c < rank; ++c) {
-    const uint32_t* other = cluster.map_shared_rank(cta_cnt, c);
-    base_gt += other[0];
-    base_eq += other[1];
-  }
-  for (int w = 0; w < warp; ++w) {
-    base_gt += w_gt[w];
-    base_eq += w_eq[w];
+  uint32_t base_gt = before_warp<NW>(w_gt, warp, lane);
+  uint32_t base_eq = before_warp<NW>(w_eq, warp, lane);
+  if constexpr (kCluster > 1) {
+    if (warp == NW - 1 && lane == 0) {
+      cta_cnt[0] = base_gt + n_gt;
+      cta_cnt[1] = base_eq + n_eq;
+    }
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) {
+      const uint32_t* other = cluster.map_shared_rank(cta_cnt, c);
+      base_gt += other[0];
+      base_eq += other[1];
+    }
   }
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int r0 = w0; r0 < w1; r0 += 32) {
     const int r = r0 + lane;
     const float m = r < w1 ? mass[r] : 0.f;
@@ -205,7 +204,7 @@ __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const 
     base_gt += __popc(bg);
     base_eq += __popc(be);
   }
-  cluster.sync();  // no CTA leaves while another may read its counts
+  if constexpr (kCluster > 1) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
 struct GatherParams {

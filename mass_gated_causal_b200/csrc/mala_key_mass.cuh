@@ -7,23 +7,31 @@
 // are recomputed tile by tile, as in the backward, and only their exponentials'
 // sums are kept.
 //
-// mala_key_mass_kernel: one CTA owns 256 keys (two tiles A, B of 128) of one (b,
-// KV head) and walks the query tiles that see them, each for all heads of the
-// GQA group. The scores are computed transposed, S^T = K Q^T: the keys are the
-// M rows, so a thread owns one key (one TMEM lane) and its sum over the queries
-// needs no exchange with other threads. K is copied into tensor memory once and
-// is the A operand of every MMA; only Q passes through shared memory, which
-// halves the operand traffic of an MMA whose both operands lie there (at N = 128
-// that traffic is as long as the MMA itself).
-//   warps 0-3  tile A: thread t = key row t; load K, then per query tile read
-//   warps 4-7  tile B  128 scores out of TMEM, hand the columns back, sum exps
-//   warp  8    producer: Q tiles by TMA and the rows' -LSE log2(e) through a ring
-//   warp  9    MMA issuer (one thread), alternating between the tiles
-// TMEM: S_A | S_B | K_A | K_B (128 + 128 + D / 2 + D / 2 columns).
+// mala_key_mass_kernel: one CTA owns NT tiles of 128 keys of one (b, KV head) and
+// walks the query tiles that see them, each for all heads of the GQA group. The
+// scores are computed transposed, S^T = K Q^T: the keys are the M rows, so a
+// thread owns one key (one TMEM lane) and its sum over the queries needs no
+// exchange with other threads. K is copied into tensor memory once and is the A
+// operand of every MMA; only Q passes through shared memory, which halves the
+// operand traffic of an MMA whose both operands lie there (at N = 128 that
+// traffic is as long as the MMA itself).
+//   warps 0 .. 8 NT - 1  compute: warps 8 x .. 8 x + 7 work on tile x, four on
+//              the first 64 queries of a query tile and four on the others; a
+//              thread reads its key's 64 scores out of TMEM, hands the columns
+//              back, and sums the exponentials
+//   warp  8 NT      producer: Q tiles by TMA and the rows' -LSE log2(e), a ring
+//   warp  8 NT + 1  MMA issuer (one thread), the tiles in turn
+// TMEM: S (NT x 128 columns) | K (NT x D / 2 columns).
 //
 // Bound: with d = 128 a 128 x 128 tile takes 512 cycles of MMA and 16,384
-// exponentials, 1,024 cycles at the special-function unit's 16 a cycle. So a
-// share of the exponentials is computed with packed FMAs instead (exp2_poly2).
+// exponentials, 1,024 cycles at the special-function unit's 16 a cycle. So three
+// of every eight pairs are computed with packed FMAs instead (exp2_poly2): a
+// pair then costs 10 cycles of either unit, 640 a tile. Sixteen compute warps of
+// 64 scores (not eight of 128) leave registers to keep both units fed.
+//
+// NT = 2 reads each Q tile once for 256 keys; NT = 1 puts two CTAs on an SM, so
+// that one's start (tensor memory, K, the first Q tile) overlaps the other's
+// walk, which is what counts when a walk is short.
 //
 // Splits: when the key tiles alone do not fill the GPU, each CTA takes
 // chunk_q query tiles and writes partial sums; mala_key_mass_join_kernel adds
@@ -39,8 +47,8 @@ struct KeyMassParams {
   int Lq, Lk;           // packed batches: the longest sequence's
   int window;           // rows that count: the last `window` (0: all)
   int chunk_q;          // query tiles a CTA takes
-  int n_chunks;         // grid: chunks per (b, KV head, key pair)
-  int n_pairs;          // key pairs that the grid covers (256 keys each)
+  int n_chunks;         // grid: chunks per (b, KV head, key block)
+  int n_blocks;         // key blocks that the grid covers (NT x 128 keys each)
   const uint16_t* k;    // [B, Lk, Hkv, d]
   const float* lse;     // [B, Hq, Lq]; packed batches: [Hq, total_q]
   const int* cu_q;      // packed batch (else null)
@@ -50,31 +58,36 @@ struct KeyMassParams {
   const float* mass_in;  // [B, Hkv, ld], nullable
   float* mass_out;
   int ld;
-  float* part;  // n_chunks > 1: [B * Hkv, n_chunks, n_pairs * 256] partial sums
+  float* part;  // n_chunks > 1: [B * Hkv, n_chunks, part_ld] partial sums
+  int part_ld;  // keys of a row of partials
   unsigned* status;
   uint64_t wait_ns;
   int stall_tile;  // test hook (-1: off): the MMA thread stalls before this item
 };
 
-template <int D>
+template <int D, int NT>
 struct KeyMassLayout {
-  static constexpr int NQ = 4;  // Q ring
+  static constexpr int NQ = NT == 2 ? 4 : 3;  // Q ring
+  static constexpr int CW = 8 * NT;           // compute warps
+  static constexpr int THREADS = (CW + 2) * 32;
   static constexpr int Q_BYTES = 128 * D * 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_LSE = OFF_Q + NQ * Q_BYTES;  // fp32 [NQ][128]
-  static constexpr int OFF_BAR = OFF_LSE + NQ * 512;
-  // q_full[NQ], q_empty[NQ], s_full[2], s_empty[2], k_ready, mma_final
-  static constexpr int N_BARS = 2 * NQ + 6;
+  static constexpr int OFF_RED = OFF_LSE + NQ * 512;    // fp32 [NT][128]: the second half's sums
+  static constexpr int OFF_BAR = OFF_RED + NT * 512;
+  // q_full[NQ], q_empty[NQ], s_full[NT], s_empty[NT], k_ready, mma_final
+  static constexpr int N_BARS = 2 * NQ + 2 * NT + 2;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
-  // at least half of an SM's shared memory: a second CTA on the SM would wait for tensor memory
-  static constexpr int ALLOC_BYTES = (BYTES > 118 * 1024 ? BYTES : 118 * 1024) + 1024;
-  static constexpr int COL_S = 0, COL_K = 256;
-  static constexpr int TMEM_COLS = 512;
+  // so much that an SM holds no more CTAs than its tensor memory does (a further one would wait for it)
+  static constexpr int LEAST = NT == 2 ? 118 * 1024 : 78 * 1024;
+  static constexpr int ALLOC_BYTES = (BYTES > LEAST ? BYTES : LEAST) + 1024;
+  static constexpr int COL_S = 0, COL_K = NT * 128;
+  static constexpr int TMEM_COLS = NT == 2 ? 512 : 256;
   static_assert(ALLOC_BYTES <= 232448, "shared memory exceeds the per-CTA limit");
 };
 
-// What a (b, KV head, key pair) has to do; the same on the device and in the join.
+// One sequence's walk over the query tiles; the same in the join.
 struct KeyMassSeq {
   int Lq, Lk, P0, first, q_off, k_off, n_qt;  // first: first row that counts; n_qt: query tiles from it
   bool ok;
@@ -131,32 +144,33 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
 
 constexpr int kMassPoly = 3;  // of every eight packed pairs, how many go through exp2_poly2
 
-template <int D>
-__global__ void __launch_bounds__(320, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
     mala_key_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const KeyMassParams p) {
-  using Lay = KeyMassLayout<D>;
-  constexpr int NQ = Lay::NQ;
+  using Lay = KeyMassLayout<D, NT>;
+  constexpr int NQ = Lay::NQ, CW = Lay::CW;
   constexpr uint32_t IDESC = idesc_bf16(128, 128, false, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + Lay::OFF_Q;
   float* sLse = reinterpret_cast<float*>(smem + Lay::OFF_LSE);
+  float* sRed = reinterpret_cast<float*>(smem + Lay::OFF_RED);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
   uint64_t* q_empty = q_full + NQ;
   uint64_t* s_full = q_empty + NQ;
-  uint64_t* s_empty = s_full + 2;
-  uint64_t* k_ready = s_empty + 2;
+  uint64_t* s_empty = s_full + NT;
+  uint64_t* k_ready = s_empty + NT;
   uint64_t* mma_final = k_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // CTA order: key pairs ascending, so the longest walks (the earliest keys) start first
+  // CTA order: key blocks ascending, so the longest walks (the earliest keys) start first
   const int chunk = static_cast<int>(blockIdx.x) % p.n_chunks;
   const int bk = (static_cast<int>(blockIdx.x) / p.n_chunks) % (p.B * p.Hkv);
-  const int pair = static_cast<int>(blockIdx.x) / (p.n_chunks * p.B * p.Hkv);
+  const int blk = static_cast<int>(blockIdx.x) / (p.n_chunks * p.B * p.Hkv);
   const int b = bk / p.Hkv, hkv = bk % p.Hkv;
-  const int k0 = pair * 256;
+  const int k0 = blk * (NT * 128);
   const KeyMassSeq sq = key_mass_seq(p, b);
   if (!sq.ok) {  // nothing of this sequence is touched
     if (threadIdx.x == 0) atomicOr(p.status, kStatusSeqTable);
@@ -166,39 +180,40 @@ __global__ void __launch_bounds__(320, 1)
   const int qt_b = k0 < sq.Lk ? min(sq.n_qt, qt_a + p.chunk_q) : 0;
   const int N = max(0, qt_b - qt_a) * p.G;  // items: (query tile, head of the group), heads fastest
   const bool direct = p.n_chunks == 1;
-  const int tid = threadIdx.x & 127, x = (warp >> 2) & 1;
-  const int key = k0 + x * 128 + tid;  // compute warps: this thread's key
-  const size_t row_at = static_cast<size_t>(bk) * p.ld;
+  // compute warps: this thread's tile, half of the queries and key
+  const int x = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3;
+  const int tid = wq * 32 + lane;
+  const int key = k0 + x * 128 + tid;
 
   auto finish = [&](float sum) {  // one key's result
     if (!direct) {
-      p.part[(static_cast<size_t>(bk) * p.n_chunks + chunk) * (p.n_pairs * 256) + key] = sum;
+      p.part[(static_cast<size_t>(bk) * p.n_chunks + chunk) * p.part_ld + key] = sum;
     } else if (key < p.ld) {
-      if (p.mass_in != nullptr && p.decay != 0.f && key < sq.P0)
-        sum = fmaf(p.decay, p.mass_in[row_at + key], sum);
-      p.mass_out[row_at + key] = key < sq.Lk ? sum : 0.f;
+      const size_t at = static_cast<size_t>(bk) * p.ld + key;
+      if (p.mass_in != nullptr && p.decay != 0.f && key < sq.P0) sum = fmaf(p.decay, p.mass_in[at], sum);
+      p.mass_out[at] = key < sq.Lk ? sum : 0.f;
     }
   };
   if (N == 0) {  // no query sees these keys (the join reads no chunk that is empty)
-    if (direct && warp < 8) finish(0.f);
+    if (direct && warp < CW && half == 0) finish(0.f);
     return;
   }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NQ; ++i) {
       mbar_init(&q_full[i], 2);
-      mbar_init(&q_empty[i], 1 + 8);
+      mbar_init(&q_empty[i], 1 + CW);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NT; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 128);
+      mbar_init(&s_empty[i], 8);
     }
-    mbar_init(k_ready, 256);
+    mbar_init(k_ready, CW);
     mbar_init(mma_final, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == CW) {
     tmem_alloc(tmem_slot, Lay::TMEM_COLS);
     tmem_relinquish();
     if (lane == 0) prefetch_tensormap(&tm_q);
@@ -209,7 +224,7 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const FailState fs{abort_flag, p.status, p.wait_ns};
 
-  if (warp == 8) {
+  if (warp == CW) {
     // ------------------------------------------------------------ producer
     const int bt = p.cu_q != nullptr ? 0 : b;
     // lane's four rows of an item's -LSE, read a whole item ahead of their use
@@ -247,7 +262,7 @@ __global__ void __launch_bounds__(320, 1)
     if (lane == 0)
       for (int n = max(0, issued - NQ); n < issued; ++n) mbar_wait_drain(&q_full[n % NQ], (n / NQ) & 1);
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == CW + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
@@ -259,7 +274,7 @@ __global__ void __launch_bounds__(320, 1)
         // loop), so the bounded wait expires and the CTA takes its abort path
         if (n == p.stall_tile && !mbar_wait(mma_final, 0, fs)) break;
         if (!mbar_wait(&q_full[st], (n / NQ) & 1, fs)) break;
-        for (int y = 0; y < 2; ++y) {
+        for (int y = 0; y < NT; ++y) {
           if (n > 0 && !mbar_wait(&s_empty[y], (n - 1) & 1, fs)) {
             ok = false;
             break;
@@ -279,58 +294,61 @@ __global__ void __launch_bounds__(320, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ compute warps
-    const int wq = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    {  // this key's row into tensor memory (A operand: two values to a column)
-      const uint32_t tK = tmem + Lay::COL_K + x * (D / 2) + lane_base;
-      const uint4* src = nullptr;
+    {  // half of this key's row into tensor memory (A operand: two values to a column)
+      constexpr int W = D / 4;  // 32-bit words of half a row
+      const uint32_t tK = tmem + Lay::COL_K + x * (D / 2) + half * W + lane_base;
+      uint32_t w[32];
       if (key < sq.Lk) {
         const size_t row = p.cu_q != nullptr ? static_cast<size_t>(sq.k_off) + key
                                              : static_cast<size_t>(b) * sq.Lk + key;
-        src = reinterpret_cast<const uint4*>(p.k + (row * p.Hkv + hkv) * D);
-      }
+        const uint4* src = reinterpret_cast<const uint4*>(p.k + (row * p.Hkv + hkv) * D + half * (D / 2));
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 v = src != nullptr ? __ldg(src + c * 8 + e) : make_uint4(0u, 0u, 0u, 0u);
+        for (int e = 0; e < W / 4; ++e) {
+          const uint4 v = __ldg(src + e);
           w[4 * e] = v.x;
           w[4 * e + 1] = v.y;
           w[4 * e + 2] = v.z;
           w[4 * e + 3] = v.w;
         }
-        tmem_st32(tK + c * 32, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] = 0u;
       }
+      __syncwarp();
+      if constexpr (W == 32) tmem_st32(tK, w);
+      else tmem_st16(tK, *reinterpret_cast<uint32_t(*)[16]>(w));
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(k_ready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_ready);
     }
-    const uint32_t tS = tmem + Lay::COL_S + x * 128 + lane_base;
+    const uint32_t tS = tmem + Lay::COL_S + x * 128 + half * 64 + lane_base;
     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
     const int kw0 = k0 + x * 128 + wq * 32;  // the warp's first key
-    const uint32_t lse_s = smem_u32(sLse);
+    const uint32_t lse_s = smem_u32(sLse) + half * 256;
     float sum = 0.f, comp = 0.f;  // compensated over the tiles: a key may be seen by 10^5 queries
     bool aborted = false;
     for (int n = 0; n < N; ++n) {
       const int st = n % NQ;
-      const int i0 = sq.first + (qt_a + n / p.G) * 128;
+      const int r0 = sq.first + (qt_a + n / p.G) * 128 + half * 64;  // this warp's first row
       if (!mbar_wait_warp(&s_full[x], n & 1, fs)) {
         aborted = true;
         break;
       }
       tc_fence_after();
-      const int pos0 = sq.P0 + i0;                                   // position of the tile's first row
-      const bool none = kw0 > pos0 + 127 || kw0 >= sq.Lk;            // no row sees a key of the warp
-      const bool plain = kw0 + 31 <= pos0 && i0 + 128 <= sq.Lq;      // every row sees every key of the warp
-      uint32_t sv[128];
+      const int pos0 = sq.P0 + r0;  // its position
+      const bool none = kw0 > pos0 + 63 || r0 >= sq.Lq || kw0 >= sq.Lk;  // no row sees a key of the warp
+      const bool plain = kw0 + 31 <= pos0 && r0 + 64 <= sq.Lq;           // every row sees every key of the warp
+      uint32_t sv[64];
       if (!none) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_at(tS + c * 32, sv + c * 32);
+        tmem_ld32_at(tS, sv);
+        tmem_ld32_at(tS + 32, sv + 32);
         tmem_ld_wait();
       }
       tc_fence_before();
-      mbar_arrive(&s_empty[x]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[x]);
       // the tile's LSEs: written before this phase of q_full completed, which the
       // MMA thread waited for before the scores; the wait makes them visible here
       if (!mbar_wait_warp(&q_full[st], (n / NQ) & 1, fs)) {
@@ -341,45 +359,41 @@ __global__ void __launch_bounds__(320, 1)
       if (!none) {
         const uint32_t la = lse_s + st * 512;
         if (plain) {
-          uint64_t acc[8];
+          uint64_t acc[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = 0ull;  // (+0, +0)
+          for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
 #pragma unroll
-          for (int j = 0; j < 128; j += 16) {
+          for (int j = 0; j < 64; j += 16) {
+            uint64_t v[8];
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              uint64_t l0, l1;
-              ld_shared_2f2(la + (j + 2 * e) * 4, l0, l1);
-              const uint64_t x0 = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])),
-                                         sl2, l0);
-              const uint64_t x1 = f2_fma(
-                  f2_pack(__uint_as_float(sv[j + 2 * e + 2]), __uint_as_float(sv[j + 2 * e + 3])), sl2, l1);
-              auto ex = [](uint64_t v, bool poly) {
-                if (poly) return exp2_poly2(v);
+            for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (j + 2 * e) * 4, v[e], v[e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (e % 2 == 1 && e < 2 * kMassPoly) {
+                v[e] = exp2_poly2(v[e]);
+              } else {
                 float lo, hi;
-                f2_unpack(v, lo, hi);
-                return f2_pack(ex2_approx(lo), ex2_approx(hi));
-              };
-              // spread over the eight pairs: e < 2 * kMassPoly picks the even ones first
-              acc[e] = f2_add(acc[e], ex(x0, e < 2 * kMassPoly));
-              acc[e + 1] = f2_add(acc[e + 1], ex(x1, e < 2 * (kMassPoly - 4)));
+                f2_unpack(v[e], lo, hi);
+                v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
+              }
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e & 3] = f2_add(acc[e & 3], v[e]);
           }
-#pragma unroll
-          for (int e = 4; e > 0; e >>= 1)
-#pragma unroll
-            for (int i = 0; i < e; ++i) acc[i] = f2_add(acc[i], acc[i + e]);
           float lo, hi;
-          f2_unpack(acc[0], lo, hi);
+          f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
           tile = lo + hi;
         } else {
-          // columns c with key <= pos0 + c and i0 + c < Lq; what is masked may be
+          // columns c with key <= pos0 + c and r0 + c < Lq; what is masked may be
           // anything (the next sequence's rows), so it is replaced, not multiplied
-          const int c_lo = key - pos0, c_hi = sq.Lq - i0;
+          const int c_lo = key - pos0, c_hi = sq.Lq - r0;
           const float s = p.scale_log2;
           float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 128; j += 4) {
+          for (int j = 0; j < 64; j += 4) {
             const float4 l = ld_shared_f4(la + j * 4);
             const float lv[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
@@ -397,12 +411,14 @@ __global__ void __launch_bounds__(320, 1)
       comp = (t - sum) - y;
       sum = t;
     }
-    if (!aborted) finish(sum);
+    if (half == 1) sRed[x * 128 + tid] = sum;
+    named_bar_sync(1, CW * 32);
+    if (half == 0 && !aborted && !abort_raised(fs)) finish(sum + sRed[x * 128 + tid]);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == CW) {
     if (lane == 0) mbar_wait_drain(mma_final, 0);
     __syncwarp();
     tc_fence_after();
@@ -411,19 +427,19 @@ __global__ void __launch_bounds__(320, 1)
 }
 
 // Adds the chunks' partial sums of each key, in order, and the earlier mass.
-// (A template only so that every translation unit may include this file.)
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads) mala_key_mass_join_kernel(const KeyMassParams p) {
+template <int NT>
+__global__ void __launch_bounds__(256) mala_key_mass_join_kernel(const KeyMassParams p) {
   const int bk = blockIdx.y, b = bk / p.Hkv;
-  const int key = blockIdx.x * kThreads + threadIdx.x;
+  const int key = blockIdx.x * 256 + threadIdx.x;
   const KeyMassSeq sq = key_mass_seq(p, b);
   if (!sq.ok || key >= p.ld) return;
   float sum = 0.f;
   if (key < sq.Lk) {
-    const int tiles = sq.n_qt - key_mass_qt0(sq, key & ~255);
+    const int tiles = sq.n_qt - key_mass_qt0(sq, key & ~(NT * 128 - 1));
     const int n = tiles > 0 ? (tiles + p.chunk_q - 1) / p.chunk_q : 0;
-    const float* src = p.part + static_cast<size_t>(bk) * p.n_chunks * (p.n_pairs * 256) + key;
-    for (int c = 0; c < n; ++c) sum += src[static_cast<size_t>(c) * (p.n_pairs * 256)];
+    const float* src = p.part + static_cast<size_t>(bk) * p.n_chunks * p.part_ld + key;
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) sum += src[static_cast<size_t>(c) * p.part_ld];
     if (p.mass_in != nullptr && p.decay != 0.f && key < sq.P0)
       sum = fmaf(p.decay, p.mass_in[static_cast<size_t>(bk) * p.ld + key], sum);
   }

@@ -9,15 +9,19 @@ using namespace mala::host;
 
 namespace {
 
+constexpr int kLongWalk = 16;  // items (query tile, head) from which a CTA owns two key tiles
+
 struct Plan {
-  int chunk_q, n_chunks, pairs;  // query tiles a CTA takes; chunks of the longest walk; key pairs
+  int tiles;              // key tiles (of 128) a CTA owns
+  int chunk_q, n_chunks;  // query tiles a CTA takes; chunks of the longest walk
+  int blocks;             // key blocks of the longest sequence
   size_t part_bytes;
 };
 
 // How the walks over the query tiles are cut. `units` (b, KV head) pairs, in
 // units of the longest sequence; `slots` of them have room in the partials.
 //
-// A CTA's walk is one key pair's query tiles. While the longest walk is at most
+// A CTA's walk is one key block's query tiles. While the longest walk is at most
 // 0.6 of an SM's share of all walks, the walks are whole: they start longest
 // first and the shorter ones even the SMs out. Above that, an SM that got the
 // longest walk would still run when the others are done, so the walks are cut
@@ -26,19 +30,38 @@ Plan plan(double units, long long slots, int G, int Lq, int Lk, int window) {
   Plan w;
   const int first = window > 0 && window < Lq ? Lq - window : 0;
   const long long n_qt = (Lq - first + 127) / 128;
-  w.pairs = (Lk + 255) / 256;
+  // two key tiles to a CTA once its walk is long enough to hide its start
+  w.tiles = n_qt * G >= kLongWalk ? 2 : 1;
+  const int keys = w.tiles * 128, slots_per_sm = 3 - w.tiles;
+  w.blocks = (Lk + keys - 1) / keys;
   const long long seen = static_cast<long long>(Lk) - Lq + first;  // position of the first row that counts
-  const long long whole = std::min<long long>(w.pairs, seen / 256 + 1), rest = w.pairs - whole;
-  const double tiles = static_cast<double>(whole) * n_qt + std::max(0.0, static_cast<double>(rest) * (n_qt - rest - 1));
-  const double share = tiles * units * G / sm_count();
+  const long long whole = std::min<long long>(w.blocks, seen / keys + 1), rest = w.blocks - whole;
+  const double walks = static_cast<double>(whole) * n_qt +
+                       std::max(0.0, static_cast<double>(rest) * (n_qt - 0.5 * w.tiles * (rest + 1)));
+  const double share = walks * units * G / (sm_count() * slots_per_sm);
   long long chunk = n_qt;
   if (static_cast<double>(n_qt) * G > 0.6 * share)
     chunk = std::max<long long>(1, std::min<long long>(n_qt, static_cast<long long>(std::ceil(0.5 * share / G))));
   w.chunk_q = static_cast<int>(chunk);
   w.n_chunks = static_cast<int>((n_qt + chunk - 1) / chunk);
   w.part_bytes =
-      w.n_chunks > 1 ? align256(static_cast<size_t>(slots) * w.n_chunks * w.pairs * 256 * sizeof(float)) : 0;
+      w.n_chunks > 1 ? align256(static_cast<size_t>(slots) * w.n_chunks * w.blocks * keys * sizeof(float)) : 0;
   return w;
+}
+
+template <int D, int NT>
+int launch(const CUtensorMap& mq, const mala::KeyMassParams& p, unsigned grid, cudaStream_t st) {
+  using Lay = mala::KeyMassLayout<D, NT>;
+  auto kern = mala::mala_key_mass_kernel<D, NT>;
+  if (set_smem(kern, Lay::ALLOC_BYTES) != MALA_OK) return MALA_ERR_CUDA;
+  kern<<<grid, Lay::THREADS, Lay::ALLOC_BYTES, st>>>(mq, p);
+  if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
+  if (p.n_chunks > 1) {
+    const dim3 jg(static_cast<unsigned>((p.ld + 255) / 256), static_cast<unsigned>(p.B) * p.Hkv);
+    mala::mala_key_mass_join_kernel<NT><<<jg, 256, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
+  }
+  return MALA_OK;
 }
 
 int check(int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale, int window, float decay, int ld) {
@@ -71,7 +94,8 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   p.chunk_q = w.chunk_q;
   p.n_chunks = w.n_chunks;
   // whole walks write the result, up to the end of its rows; chunks write partials
-  p.n_pairs = w.n_chunks > 1 ? w.pairs : (ld + 255) / 256;
+  p.n_blocks = w.n_chunks > 1 ? w.blocks : (ld + w.tiles * 128 - 1) / (w.tiles * 128);
+  p.part_ld = w.blocks * w.tiles * 128;
   p.k = static_cast<const uint16_t*>(k);
   p.lse = lse;
   p.cu_q = cu_q;
@@ -88,28 +112,14 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   if (!p.status) return MALA_ERR_CUDA;
   p.wait_ns = wait_limit_ns();
   p.stall_tile = stall_tile();
-  const long long grid = static_cast<long long>(p.n_pairs) * slots * w.n_chunks;
+  const long long grid = static_cast<long long>(p.n_blocks) * slots * w.n_chunks;
   if (grid >= (1ll << 31)) return MALA_ERR_UNSUPPORTED;
   CUtensorMap mq;
   if (!make_bshd_map(&mq, q, packed ? 1 : B, packed ? total_q : Lq, Hq, d, 128)) return MALA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned g = static_cast<unsigned>(grid);
-  if (d == 128) {
-    auto kern = mala::mala_key_mass_kernel<128>;
-    if (set_smem(kern, mala::KeyMassLayout<128>::ALLOC_BYTES) != MALA_OK) return MALA_ERR_CUDA;
-    kern<<<g, 320, mala::KeyMassLayout<128>::ALLOC_BYTES, st>>>(mq, p);
-  } else {
-    auto kern = mala::mala_key_mass_kernel<64>;
-    if (set_smem(kern, mala::KeyMassLayout<64>::ALLOC_BYTES) != MALA_OK) return MALA_ERR_CUDA;
-    kern<<<g, 320, mala::KeyMassLayout<64>::ALLOC_BYTES, st>>>(mq, p);
-  }
-  if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
-  if (w.n_chunks > 1) {
-    const dim3 jg(static_cast<unsigned>((ld + 255) / 256), static_cast<unsigned>(slots));
-    mala::mala_key_mass_join_kernel<256><<<jg, 256, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
-  }
-  return MALA_OK;
+  if (d == 128) return w.tiles == 2 ? launch<128, 2>(mq, p, g, st) : launch<128, 1>(mq, p, g, st);
+  return w.tiles == 2 ? launch<64, 2>(mq, p, g, st) : launch<64, 1>(mq, p, g, st);
 }
 
 }  // namespace
