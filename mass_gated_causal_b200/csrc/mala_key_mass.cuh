@@ -38,6 +38,8 @@
 // them in a fixed order, so results do not depend on the schedule.
 #pragma once
 
+#include <type_traits>
+
 #include "mala_ptx.cuh"
 
 namespace mala {
@@ -142,7 +144,7 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
                  __uint_as_float(__float_as_uint(rhi) + (__float_as_uint(mhi) << 23)));
 }
 
-constexpr int kMassPoly = 3;  // of every eight packed pairs, how many go through exp2_poly2
+constexpr int kMassPoly = 1;  // of every eight packed pairs, how many go through exp2_poly2
 
 template <int D, int NT>
 __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
@@ -228,8 +230,8 @@ __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
     // ------------------------------------------------------------ producer
     const int bt = p.cu_q != nullptr ? 0 : b;
     // lane's four rows of an item's -LSE, read a whole item ahead of their use
-    auto load_lse = [&](int n, float (&v)[4]) {
-      const int i0 = sq.first + (qt_a + n / p.G) * 128, hq = hkv * p.G + n % p.G;
+    auto load_lse = [&](int i0, int g, float (&v)[4]) {
+      const int hq = hkv * p.G + g;
       const float* src = p.cu_q != nullptr ? p.lse + static_cast<size_t>(hq) * p.total_q + sq.q_off
                                            : p.lse + (static_cast<size_t>(b) * p.Hq + hq) * sq.Lq;
 #pragma unroll
@@ -239,17 +241,18 @@ __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
       }
     };
     float cur[4], nxt[4];
-    load_lse(0, cur);
-    int issued = 0;
+    int i0 = sq.first + qt_a * 128, g = 0, st = 0, issued = 0;
+    uint32_t par = 1;
+    load_lse(i0, 0, cur);
     for (int n = 0; n < N; ++n) {
-      const int st = n % NQ;
-      if (n + 1 < N) load_lse(n + 1, nxt);
-      if (n >= NQ && !mbar_wait_warp(&q_empty[st], ((n / NQ) - 1) & 1, fs)) break;
+      const int g_n = g + 1 == p.G ? 0 : g + 1, i0_n = g_n == 0 ? i0 + 128 : i0;
+      if (n + 1 < N) load_lse(i0_n, g_n, nxt);
+      if (n >= NQ && !mbar_wait_warp(&q_empty[st], par, fs)) break;
       if (lane == 0) {
-        const int i0 = sq.first + (qt_a + n / p.G) * 128, hq = hkv * p.G + n % p.G;
         mbar_arrive_expect_tx(&q_full[st], Lay::Q_BYTES);
         for (int h = 0; h < D / 64; ++h)
-          tma_load_4d(&tm_q, &q_full[st], sQ + st * Lay::Q_BYTES + h * 16384, h * 64, hq, sq.q_off + i0, bt);
+          tma_load_4d(&tm_q, &q_full[st], sQ + st * Lay::Q_BYTES + h * 16384, h * 64, hkv * p.G + g, sq.q_off + i0,
+                      bt);
       }
       issued = n + 1;
 #pragma unroll
@@ -258,6 +261,12 @@ __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
       if (lane == 0) mbar_arrive(&q_full[st]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) cur[e] = nxt[e];
+      g = g_n;
+      i0 = i0_n;
+      if (++st == NQ) {
+        st = 0;
+        par ^= 1u;  // the first wait for a slot is for its first release (phase 0)
+      }
     }
     if (lane == 0)
       for (int n = max(0, issued - NQ); n < issued; ++n) mbar_wait_drain(&q_full[n % NQ], (n / NQ) & 1);
@@ -329,87 +338,96 @@ __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
     const uint32_t lse_s = smem_u32(sLse) + half * 256;
     float sum = 0.f, comp = 0.f;  // compensated over the tiles: a key may be seen by 10^5 queries
     bool aborted = false;
+    // one 64 x 1 strip of an item: the sum of this key's weights over the strip's queries.
+    // kPlain: every row of the strip counts and sees every key of the warp.
+    auto strip = [&](auto plain_c, uint32_t la, int c_lo, int c_hi) -> float {
+      constexpr bool kPlain = decltype(plain_c)::value;
+      uint64_t acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
+#pragma unroll
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t sv[32];
+        tmem_ld32(tS + c0, sv);
+        tmem_ld_wait();
+        if (c0 == 32) {  // the scores are out of TMEM: its columns go back to the MMA issuer
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[x]);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 16) {
+          uint64_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (c0 + j + 2 * e) * 4, v[e], v[e + 1]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (kPlain && e % 2 == 1 && e < 2 * kMassPoly) {
+              v[e] = exp2_poly2(v[e]);
+            } else {
+              float lo, hi;
+              f2_unpack(v[e], lo, hi);
+              if (!kPlain) {  // columns c with key <= position of row c, rows below Lq. What is masked may be
+                              // anything (the next sequence's rows), so it is replaced, not multiplied
+                const int c = c0 + j + 2 * e;
+                lo = c >= c_lo && c < c_hi ? lo : -INFINITY;
+                hi = c + 1 >= c_lo && c + 1 < c_hi ? hi : -INFINITY;
+              }
+              v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e & 3] = f2_add(acc[e & 3], v[e]);
+        }
+      }
+      float lo, hi;
+      f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
+      return lo + hi;
+    };
+    int st = 0, g = 0;
+    uint32_t q_par = 0, s_par = 0;
+    int r0 = sq.first + qt_a * 128 + half * 64;  // this warp's first row of the item
     for (int n = 0; n < N; ++n) {
-      const int st = n % NQ;
-      const int r0 = sq.first + (qt_a + n / p.G) * 128 + half * 64;  // this warp's first row
-      if (!mbar_wait_warp(&s_full[x], n & 1, fs)) {
+      if (!mbar_wait_warp(&s_full[x], s_par, fs)) {
+        aborted = true;
+        break;
+      }
+      // the tile's LSEs: written before this phase of q_full completed, which the
+      // MMA thread waited for before the scores; the wait makes them visible here
+      if (!mbar_wait_warp(&q_full[st], q_par, fs)) {
         aborted = true;
         break;
       }
       tc_fence_after();
-      const int pos0 = sq.P0 + r0;  // its position
-      const bool none = kw0 > pos0 + 63 || r0 >= sq.Lq || kw0 >= sq.Lk;  // no row sees a key of the warp
-      const bool plain = kw0 + 31 <= pos0 && r0 + 64 <= sq.Lq;           // every row sees every key of the warp
-      uint32_t sv[64];
-      if (!none) {
-        tmem_ld32_at(tS, sv);
-        tmem_ld32_at(tS + 32, sv + 32);
-        tmem_ld_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[x]);
-      // the tile's LSEs: written before this phase of q_full completed, which the
-      // MMA thread waited for before the scores; the wait makes them visible here
-      if (!mbar_wait_warp(&q_full[st], (n / NQ) & 1, fs)) {
-        aborted = true;
-        break;
-      }
+      const int pos0 = sq.P0 + r0;  // position of the first row
+      const uint32_t la = lse_s + st * 512;
       float tile = 0.f;
-      if (!none) {
-        const uint32_t la = lse_s + st * 512;
-        if (plain) {
-          uint64_t acc[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
-#pragma unroll
-          for (int j = 0; j < 64; j += 16) {
-            uint64_t v[8];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (j + 2 * e) * 4, v[e], v[e + 1]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (e % 2 == 1 && e < 2 * kMassPoly) {
-                v[e] = exp2_poly2(v[e]);
-              } else {
-                float lo, hi;
-                f2_unpack(v[e], lo, hi);
-                v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e & 3] = f2_add(acc[e & 3], v[e]);
-          }
-          float lo, hi;
-          f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
-          tile = lo + hi;
-        } else {
-          // columns c with key <= pos0 + c and r0 + c < Lq; what is masked may be
-          // anything (the next sequence's rows), so it is replaced, not multiplied
-          const int c_lo = key - pos0, c_hi = sq.Lq - r0;
-          const float s = p.scale_log2;
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const float4 l = ld_shared_f4(la + j * 4);
-            const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool live = j + e >= c_lo && j + e < c_hi;
-              part[e] += ex2_approx(live ? fmaf(__uint_as_float(sv[j + e]), s, lv[e]) : -INFINITY);
-            }
-          }
-          tile = (part[0] + part[1]) + (part[2] + part[3]);
-        }
+      if (kw0 + 31 <= pos0 && r0 + 64 <= sq.Lq) {
+        tile = strip(std::true_type(), la, 0, 0);
+      } else if (kw0 <= pos0 + 63 && r0 < sq.Lq && kw0 < sq.Lk) {
+        tile = strip(std::false_type(), la, key - pos0, sq.Lq - r0);
+      } else {  // no row sees a key of the warp
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[x]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[st]);  // this warp has read the LSEs
       const float y = tile - comp, t = sum + y;
       comp = (t - sum) - y;
       sum = t;
+      s_par ^= 1u;
+      if (++st == NQ) {
+        st = 0;
+        q_par ^= 1u;
+      }
+      if (++g == p.G) {
+        g = 0;
+        r0 += 128;
+      }
     }
     if (half == 1) sRed[x * 128 + tid] = sum;
     named_bar_sync(1, CW * 32);

@@ -4,12 +4,21 @@
 
 #include "mala_host.h"
 #include "mala_key_mass.cuh"
+#include "mala_key_mass_window.cuh"
 
 using namespace mala::host;
 
 namespace {
 
 constexpr int kLongWalk = 16;  // items (query tile, head) from which a CTA owns two key tiles
+
+// Columns of Q that mala_key_mass_window_kernel holds (rows of all heads, each
+// head's rounded up to 8), or 0 if it does not take the call.
+int window_cols(int G, int Lq, int window) {
+  const int rows = window > 0 ? std::min(window, Lq) : Lq;
+  const int pad = (std::min(rows, 512) + 7) & ~7;
+  return pad <= 256 && static_cast<long long>(pad) * G <= mala::kWinMaxCols ? pad * G : 0;
+}
 
 struct Plan {
   int tiles;              // key tiles (of 128) a CTA owns
@@ -27,7 +36,8 @@ struct Plan {
 // longest walk would still run when the others are done, so the walks are cut
 // into chunks of half a share.
 Plan plan(double units, long long slots, int G, int Lq, int Lk, int window) {
-  Plan w;
+  Plan w = {};
+  if (window_cols(G, Lq, window) > 0) return w;  // Q fits in shared memory: the keys stream past it
   const int first = window > 0 && window < Lq ? Lq - window : 0;
   const long long n_qt = (Lq - first + 127) / 128;
   // two key tiles to a CTA once its walk is long enough to hide its start
@@ -64,6 +74,50 @@ int launch(const CUtensorMap& mq, const mala::KeyMassParams& p, unsigned grid, c
   return MALA_OK;
 }
 
+template <int D, int kCols>
+int launch_window(const CUtensorMap& mq, const CUtensorMap& mk, mala::WinParams wp, cudaStream_t st) {
+  using Lay = mala::WinLayout<D, kCols>;
+  wp.k_stages = std::min(Lay::MAX_STAGES, (232448 - Lay::bytes(wp.col_blocks, 0)) / Lay::K_BYTES);
+  const int bytes = Lay::bytes(wp.col_blocks, wp.k_stages);
+  auto kern = mala::mala_key_mass_window_kernel<D, kCols>;
+  if (set_smem(kern, bytes) != MALA_OK) return MALA_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(wp.m.B) * wp.m.Hkv * wp.parts;
+  kern<<<grid, Lay::THREADS, bytes, st>>>(mq, mk, wp);
+  return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
+}
+
+template <int D>
+int run_window(const void* q, const void* k, const mala::KeyMassParams& p, int cols, cudaStream_t st) {
+  const bool packed = p.cu_q != nullptr;
+  const int tb = packed ? 1 : p.B, tq = packed ? p.total_q : p.Lq, tk = packed ? p.total_k : p.Lk;
+  mala::WinParams wp = {};
+  wp.m = p;
+  wp.rows_pad = cols / p.G;
+  wp.col_blocks = cols > 256 ? 2 : 1;
+  const int block = ((cols + wp.col_blocks - 1) / wp.col_blocks + 63) & ~63;
+  // CTAs per (b, KV head): the count whose waves of one CTA per SM take the fewest key tiles in all
+  const long long units = static_cast<long long>(p.B) * p.Hkv, tiles = (p.Lk + 127) / 128;
+  const long long sms = sm_count();
+  long long best = -1;
+  for (long long s = 1; s <= std::min(tiles, sms); ++s) {
+    const long long per = (tiles + s - 1) / s, waves = (units * s + sms - 1) / sms;
+    const long long cost = waves * (per + 3);  // a CTA's start takes about as long as three tiles
+    if (best < 0 || cost < best) {
+      best = cost;
+      wp.parts = static_cast<int>(s);
+    }
+  }
+  CUtensorMap mq, mk;
+  if (!make_bshd_map(&mq, q, tb, tq, p.Hq, D, wp.rows_pad) || !make_bshd_map(&mk, k, tb, tk, p.Hkv, D, 128))
+    return MALA_ERR_CUDA;
+  switch (block) {
+    case 64: return launch_window<D, 64>(mq, mk, wp, st);
+    case 128: return launch_window<D, 128>(mq, mk, wp, st);
+    case 192: return launch_window<D, 192>(mq, mk, wp, st);
+    default: return launch_window<D, 256>(mq, mk, wp, st);
+  }
+}
+
 int check(int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale, int window, float decay, int ld) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lk < Lq || Hq % Hkv != 0) return MALA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || !(decay >= 0.f) || !std::isfinite(decay)) return MALA_ERR_INVALID_ARG;
@@ -94,7 +148,7 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   p.chunk_q = w.chunk_q;
   p.n_chunks = w.n_chunks;
   // whole walks write the result, up to the end of its rows; chunks write partials
-  p.n_blocks = w.n_chunks > 1 ? w.blocks : (ld + w.tiles * 128 - 1) / (w.tiles * 128);
+  if (w.tiles > 0) p.n_blocks = w.n_chunks > 1 ? w.blocks : (ld + w.tiles * 128 - 1) / (w.tiles * 128);
   p.part_ld = w.blocks * w.tiles * 128;
   p.k = static_cast<const uint16_t*>(k);
   p.lse = lse;
@@ -112,6 +166,10 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   if (!p.status) return MALA_ERR_CUDA;
   p.wait_ns = wait_limit_ns();
   p.stall_tile = stall_tile();
+  if (const int cols = window_cols(p.G, Lq, window)) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return d == 128 ? run_window<128>(q, k, p, cols, st) : run_window<64>(q, k, p, cols, st);
+  }
   const long long grid = static_cast<long long>(p.n_blocks) * slots * w.n_chunks;
   if (grid >= (1ll << 31)) return MALA_ERR_UNSUPPORTED;
   CUtensorMap mq;

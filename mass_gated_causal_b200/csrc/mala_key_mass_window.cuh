@@ -1,0 +1,332 @@
+// mala_key_mass_window.cuh -- key mass of a few query rows against a long cache
+// (the last rows of a prompt, a short chunk).
+//
+// Mathematics as in mala_key_mass.cuh. With G x W rows in all (W rows that
+// count, G heads of the group) small enough for shared memory, the roles turn:
+// Q stays, K streams. One CTA takes one (b, KV head) and a run of its key tiles;
+// Q of all G heads is one operand of up to 512 columns, loaded once, so a key
+// tile costs its K and one MMA of N = kCols columns per half-row step, and no
+// start-up per key block (a walk per 128 keys, as in mala_key_mass_kernel, spent
+// 10 us on four query tiles).
+//   warps 0-15  compute: warp w owns the keys 32 (w % 4) .. + 31 of a tile and the
+//               columns (w / 4) kCols / 4 .. of a block; the four column groups'
+//               sums meet in shared memory, and group 0 writes the result
+//   warp  16    producer: Q once, K tiles through a ring
+//   warp  17    MMA issuer (one thread): S^T = K Q^T, two TMEM buffers in turn
+// Columns past a head's rows hold zeros in Q and -infinity in place of -LSE, so
+// they add nothing (at most 2^-126). Bound: G x W exponentials per key on the special-function
+// unit (at 256 columns 2,048 cycles a tile against 760 for reading K at the HBM
+// rate), which shares them with the FMA pipes (exp2_poly2).
+#pragma once
+
+#include "mala_key_mass.cuh"
+
+namespace mala {
+
+constexpr int kWinMaxCols = 512;  // query rows of all heads that a CTA holds
+constexpr int kWinPoly = 2;       // of every eight packed pairs, how many go through exp2_poly2
+
+struct WinParams {
+  KeyMassParams m;  // n_blocks, n_chunks, chunk_q and part are not used
+  int rows_pad;     // W rounded up to 8: a head's columns
+  int col_blocks;   // blocks of kCols columns (1 or 2)
+  int parts;        // CTAs per (b, KV head)
+  int k_stages;     // K ring
+};
+
+template <int D, int kCols>
+struct WinLayout {
+  static constexpr int THREADS = 18 * 32;
+  static constexpr int K_BYTES = 128 * D * 2;
+  static constexpr int MAX_STAGES = 4;
+  static constexpr int AHEAD = 6;  // tiles that the earlier masses are fetched ahead (a tile may take 0.3 us)
+  // lse [512], pos [512], red [2][4][128], earlier masses [AHEAD + 1][128], then barriers
+  static constexpr int OFF_LSE = 0;
+  static constexpr int OFF_POS = OFF_LSE + kWinMaxCols * 4;
+  static constexpr int OFF_RED = OFF_POS + kWinMaxCols * 4;
+  static constexpr int OFF_OLD = OFF_RED + 2 * 4 * 128 * 4;
+  static constexpr int OFF_BAR = OFF_OLD + (AHEAD + 1) * 128 * 4;
+  // k_full[4], k_empty[4], s_full[2], s_empty[2], q_full, q_ready, mma_final
+  static constexpr int N_BARS = 2 * MAX_STAGES + 4 + 3;
+  static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+  static constexpr int OFF_Q = (OFF_MISC + 16 + 1023) & ~1023;
+  static constexpr int q_bytes(int col_blocks) { return col_blocks * kCols * D * 2; }
+  static constexpr int bytes(int col_blocks, int stages) {
+    return OFF_Q + q_bytes(col_blocks) + stages * K_BYTES + 1024;
+  }
+};
+
+template <int D, int kCols>
+__global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
+    mala_key_mass_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                                const WinParams wp) {
+  using Lay = WinLayout<D, kCols>;
+  const KeyMassParams& p = wp.m;
+  constexpr uint32_t IDESC = idesc_bf16(128, kCols, false, false);
+  constexpr int CG = kCols / 4;  // columns of a block per compute warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* sLse = reinterpret_cast<float*>(smem + Lay::OFF_LSE);
+  int* sPos = reinterpret_cast<int*>(smem + Lay::OFF_POS);
+  float* sRed = reinterpret_cast<float*>(smem + Lay::OFF_RED);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
+  uint64_t* k_empty = k_full + Lay::MAX_STAGES;
+  uint64_t* s_full = k_empty + Lay::MAX_STAGES;
+  uint64_t* s_empty = s_full + 2;
+  uint64_t* q_full = s_empty + 2;
+  uint64_t* q_ready = q_full + 1;
+  uint64_t* mma_final = q_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  uint8_t* sQ = smem + Lay::OFF_Q;
+  const int cols = wp.col_blocks * kCols;  // columns in all
+  uint8_t* sK = sQ + cols * D * 2;
+  const int NK = wp.k_stages;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bk = static_cast<int>(blockIdx.x) % (p.B * p.Hkv), part = static_cast<int>(blockIdx.x) / (p.B * p.Hkv);
+  const int b = bk / p.Hkv, hkv = bk % p.Hkv;
+  const KeyMassSeq sq = key_mass_seq(p, b);
+  if (!sq.ok) {  // nothing of this sequence is touched
+    if (threadIdx.x == 0 && part == 0) atomicOr(p.status, kStatusSeqTable);
+    return;
+  }
+  const int rows = sq.Lq - sq.first;  // rows of a head that count (<= rows_pad)
+  const int n_tiles = (sq.Lk + 127) / 128;
+  const int per = (n_tiles + wp.parts - 1) / wp.parts;
+  const int t0 = min(part * per, n_tiles), T = min(per, n_tiles - t0);
+  const size_t row_at = static_cast<size_t>(bk) * p.ld;
+  // the entries past the keys, by the last part
+  if (part == wp.parts - 1)
+    for (int j = sq.Lk + static_cast<int>(threadIdx.x); j < p.ld; j += Lay::THREADS) p.mass_out[row_at + j] = 0.f;
+  if (T <= 0) return;
+  if (rows <= 0) {  // a sequence without queries: its keys keep what they have
+    for (int j = t0 * 128 + static_cast<int>(threadIdx.x); j < min((t0 + T) * 128, sq.Lk); j += Lay::THREADS)
+      p.mass_out[row_at + j] =
+          p.mass_in != nullptr && p.decay != 0.f && j < sq.P0 ? p.decay * p.mass_in[row_at + j] : 0.f;
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Lay::MAX_STAGES; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 16);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_ready, 16);
+    mbar_init(mma_final, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+    if (lane == 0) {
+      prefetch_tensormap(&tm_q);
+      prefetch_tensormap(&tm_k);
+    }
+  }
+  for (int c = threadIdx.x; c < cols; c += Lay::THREADS) {
+    const int g = c / wp.rows_pad, r = c % wp.rows_pad;
+    const int i = sq.first + r;
+    float l = -INFINITY;
+    if (g < p.G && r < rows) {
+      const int hq = hkv * p.G + g;
+      l = -1.4426950408889634f * __ldg(p.cu_q != nullptr ? p.lse + static_cast<size_t>(hq) * p.total_q + sq.q_off + i
+                                                         : p.lse + (static_cast<size_t>(b) * p.Hq + hq) * sq.Lq + i);
+    }
+    sLse[c] = l;
+    sPos[c] = sq.P0 + i;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const FailState fs{abort_flag, p.status, p.wait_ns};
+
+  if (warp == 16) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const int bt = p.cu_q != nullptr ? 0 : b;
+      mbar_arrive_expect_tx(q_full, p.G * wp.rows_pad * D * 2);
+      for (int g = 0; g < p.G; ++g)
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(&tm_q, q_full, sQ + h * (cols * 128) + g * wp.rows_pad * 128, h * 64, hkv * p.G + g,
+                      sq.q_off + sq.first, bt);
+      int st = 0, issued = 0;
+      uint32_t par = 1;
+      for (int t = 0; t < T; ++t) {
+        if (t >= NK && !mbar_wait(&k_empty[st], par, fs)) break;
+        mbar_arrive_expect_tx(&k_full[st], Lay::K_BYTES);
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(&tm_k, &k_full[st], sK + st * Lay::K_BYTES + h * 16384, h * 64, hkv,
+                      sq.k_off + (t0 + t) * 128, bt);
+        issued = t + 1;
+        if (++st == NK) {
+          st = 0;
+          par ^= 1u;  // the first wait for a slot is for its first release (phase 0)
+        }
+      }
+      mbar_wait_drain(q_full, 0);
+      for (int t = max(0, issued - NK); t < issued; ++t) mbar_wait_drain(&k_full[t % NK], (t / NK) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 17) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      bool ok = mbar_wait(q_ready, 0, fs);
+      int st = 0, n = 0;
+      uint32_t par = 0;
+      for (int t = 0; ok && t < T; ++t) {
+        // test hook: wait on a barrier only this thread completes (after the
+        // loop), so the bounded wait expires and the CTA takes its abort path
+        if (t == p.stall_tile && !mbar_wait(mma_final, 0, fs)) break;
+        if (!mbar_wait(&k_full[st], par, fs)) break;
+        for (int y = 0; y < wp.col_blocks; ++y, ++n) {
+          if (n >= 2 && !mbar_wait(&s_empty[n & 1], ((n >> 1) - 1) & 1, fs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ss(tmem + (n & 1) * 256, sdesc_add(dK, st * Lay::K_BYTES + (kk >> 2) * 16384 + (kk & 3) * 32),
+                         sdesc_add(dQ, (kk >> 2) * (cols * 128) + y * (kCols * 128) + (kk & 3) * 32), IDESC,
+                         kk > 0 ? 1u : 0u);
+          umma_commit(&s_full[n & 1]);
+        }
+        if (ok) umma_commit(&k_empty[st]);
+        if (++st == NK) {
+          st = 0;
+          par ^= 1u;
+        }
+      }
+      umma_commit(mma_final);  // completes once every MMA above has finished
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ compute warps
+    const int wq = warp & 3, cg = warp >> 2;
+    const int tid = wq * 32 + lane;  // key within the tile
+    bool aborted = !mbar_wait_warp(q_full, 0, fs);
+    // rows that do not count: of a head past its rows (another sequence's, perhaps), and past the last head
+    for (int i = warp * 32 + lane; i < cols * (D / 8); i += 16 * 32) {
+      const int c = i / (D / 8), ch = i % (D / 8);
+      if (c / wp.rows_pad >= p.G || c % wp.rows_pad >= rows)
+        st_shared_v4(smem_u32(sQ) + (ch >> 3) * (cols * 128) + sw128_offset(c, ch & 7), 0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_ready);
+
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
+    const uint32_t lse_a = smem_u32(sLse) + cg * CG * 4;
+    const int p_min = sq.P0 + sq.first;  // position of the first row that counts
+    // Group 0 adds the earlier masses: each thread copies its key's into its own slot of a ring
+    // in shared memory, AHEAD tiles before it reads it. A sequence's own tokens start from 0.
+    constexpr int AHEAD = Lay::AHEAD;
+    const bool has_old = cg == 0 && p.mass_in != nullptr && p.decay != 0.f;
+    float* sOld = reinterpret_cast<float*>(smem + Lay::OFF_OLD) + tid;
+    auto fetch_old = [&](int t, int slot) {
+      const int key = (t0 + t) * 128 + tid;
+      if (has_old && t < T && key < sq.P0) cp_async_4(smem_u32(sOld + slot * 128), p.mass_in + row_at + key);
+      cp_async_commit();  // one group a tile, empty or not, so that the counting holds
+    };
+    for (int t = 0; t < AHEAD; ++t) fetch_old(t, t);
+    int slot = 0;
+    int n = 0;
+    for (int t = 0; t < T; ++t) {
+      const int k0 = (t0 + t) * 128, key = k0 + tid;
+      const bool mine = cg == 0 && key < sq.Lk;
+      fetch_old(t + AHEAD, slot == 0 ? AHEAD : slot - 1);
+      const bool plain = k0 + 127 <= p_min;  // every row sees every key
+      float sum = 0.f;
+      for (int y = 0; y < wp.col_blocks; ++y, ++n) {
+        if (!aborted) aborted = !mbar_wait_warp(&s_full[n & 1], (n >> 1) & 1, fs);
+        if (aborted) continue;  // the barriers below are still met
+        tc_fence_after();
+        const uint32_t tS = tmem + (n & 1) * 256 + cg * CG + lane_base;
+        const uint32_t la = lse_a + y * kCols * 4;
+        uint64_t acc[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
+#pragma unroll
+        for (int c0 = 0; c0 < CG; c0 += 32) {
+          constexpr int kLast = (CG - 1) / 32 * 32;
+          uint32_t sv[32];
+          if (CG - c0 >= 32) tmem_ld32(tS + c0, sv);
+          else tmem_ld16(tS + c0, *reinterpret_cast<uint32_t(*)[16]>(sv));
+          tmem_ld_wait();
+          if (c0 == kLast) {  // the block is out of TMEM: its columns go back to the MMA issuer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[n & 1]);
+          }
+#pragma unroll
+          for (int j = 0; j < 32 && c0 + j < CG; j += 16) {
+            uint64_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (c0 + j + 2 * e) * 4, v[e], v[e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
+            if (plain) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (e % 2 == 1 && e < 2 * kWinPoly) {
+                  v[e] = exp2_poly2(v[e]);
+                } else {
+                  float lo, hi;
+                  f2_unpack(v[e], lo, hi);
+                  v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
+                }
+              }
+            } else {
+              const int* pos = sPos + y * kCols + cg * CG + c0 + j;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float lo, hi;
+                f2_unpack(v[e], lo, hi);
+                lo = key <= pos[2 * e] ? lo : -INFINITY;
+                hi = key <= pos[2 * e + 1] ? hi : -INFINITY;
+                v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e & 3] = f2_add(acc[e & 3], v[e]);
+          }
+        }
+        float lo, hi;
+        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
+        sum += lo + hi;
+      }
+      float* red = sRed + (t & 1) * 512;
+      red[cg * 128 + tid] = sum;
+      named_bar_sync(1, 512);  // the next tile writes the other half of sRed
+      if (mine && !aborted && !abort_raised(fs)) {
+        float m = (red[tid] + red[128 + tid]) + (red[256 + tid] + red[384 + tid]);
+        cp_async_wait<AHEAD>();
+        if (has_old && key < sq.P0) m = fmaf(p.decay, sOld[slot * 128], m);
+        p.mass_out[row_at + key] = m;
+      }
+      slot = slot == AHEAD ? 0 : slot + 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    if (lane == 0) mbar_wait_drain(mma_final, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace mala
