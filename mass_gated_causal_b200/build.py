@@ -1,4 +1,5 @@
-"""Build the MALA CUDA library (sm_100a) in-tree: mass_gated_causal_b200/libmala.so.
+"""Build the MALA CUDA library (sm_100a) in-tree: mass_gated_causal_b200/libmala.so,
+and the torch side of some of its calls, mala_torch.so (csrc/mala_torch.cpp).
 
 nvcc cross-compiles for sm_100a without a GPU. Every csrc/*.cu is one
 translation unit, compiled to an object of its own (several at a time, and only
@@ -19,6 +20,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmala.so")
+TORCH_SRC = os.path.join(SRC_DIR, "mala_torch.cpp")
+TORCH_LIB = os.path.join(HERE, "mala_torch.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -52,7 +55,26 @@ def _stale(out, files) -> bool:
 
 
 def needs_build() -> bool:
-    return any(_stale(LIB, _files_of(s)) for s in sources())
+    return any(_stale(LIB, _files_of(s)) for s in sources()) or _stale(TORCH_LIB, _files_of(TORCH_SRC))
+
+
+def _build_torch_side() -> None:
+    """mala_torch.so: a CPython module against torch's headers that calls libmala.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    home = os.path.dirname(os.path.dirname(NVCC))
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += ["-isystem" + d for d in cpp_extension.include_paths() + [os.path.join(home, "include"),
+                                                                     sysconfig.get_paths()["include"]]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd += [TORCH_SRC, "-o", tmp, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", LIB,
+            "-Wl,-rpath,$ORIGIN"]
+    subprocess.check_call(cmd)
+    os.replace(tmp, TORCH_LIB)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -72,8 +94,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(len(sources()), os.cpu_count() or 1)) as pool:
         objs = list(pool.map(compile_one, sources()))
     tmp = LIB + f".tmp{os.getpid()}"
-    subprocess.check_call([NVCC] + FLAGS + ["-shared"] + objs + ["-o", tmp])
+    subprocess.check_call([NVCC] + FLAGS + ["-shared", "-Xlinker", "-soname=libmala.so"] + objs + ["-o", tmp])
     os.replace(tmp, LIB)
+    if force or _stale(TORCH_LIB, _files_of(TORCH_SRC)):
+        _build_torch_side()
     return LIB
 
 

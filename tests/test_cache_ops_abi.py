@@ -211,12 +211,12 @@ def test_binding_refuses_cpu_tensors():
     (lambda x: x.view(1, 1, 24, 128), (1, 24, 128, 0, 128)),
 ])
 def test_rows_of_a_strided_tensor(make, want):
-    assert mala._rows("test", "x", make(torch.zeros(4 * 6 * 128))) == want
+    assert mala._load_native().rows(make(torch.zeros(4 * 6 * 128))) == want
 
 
 def test_rows_refuses_tokens_at_two_strides():
     x = torch.zeros(4, 3, 6, 128)[:, :2]
     with pytest.raises(ValueError):
-        mala._rows("test", "x", x)
+        mala._load_native().rows(x)
     with pytest.raises(ValueError):
-        mala._rows("test", "x", torch.zeros(4, 128, 6).transpose(1, 2))
+        mala._load_native().rows(torch.zeros(4, 128, 6).transpose(1, 2))
