@@ -64,6 +64,7 @@ int launch_rope_u(const mala::RopeParams& p, int rows, cudaStream_t st) {
   if (grid >= (1ll << 31)) return MALA_ERR_UNSUPPORTED;
   const unsigned g = static_cast<unsigned>(grid);
   if (rows >= 4) mala::mala_rope_kernel<D, kAdjacent, kPaged, 4><<<g, mala::kRopeThreads, 0, st>>>(p);
+  else if (rows >= 2) mala::mala_rope_kernel<D, kAdjacent, kPaged, 2><<<g, mala::kRopeThreads, 0, st>>>(p);
   else mala::mala_rope_kernel<D, kAdjacent, kPaged, 1><<<g, mala::kRopeThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
 }
@@ -71,11 +72,13 @@ int launch_rope_u(const mala::RopeParams& p, int rows, cudaStream_t st) {
 template <bool kPaged>
 int launch_rope(mala::RopeParams p, int d, bool adjacent, cudaStream_t st) {
   // Rows (heads) per thread: one while the rows of all tokens do not fill the
-  // GPU twice, then up to 12 so that a thread's sines serve several heads.
+  // GPU twice, then up to 12 so that a thread's sines serve several heads, in
+  // whole groups of the loads a thread has in flight (1, 2, 4, 8, 12).
   const long long rows = p.heads[0] + p.heads[1] + p.heads[2];
   const long long threads = p.T * rows * (d / 16);
   const long long fill = static_cast<long long>(sm_count()) * 2048 * 2;
-  const int per = static_cast<int>(std::min<long long>(std::max<long long>(threads / fill, 1), 12));
+  int per = static_cast<int>(std::min<long long>(std::max<long long>(threads / fill, 1), 12));
+  per = per >= 4 ? per / 4 * 4 : per >= 2 ? 2 : 1;
   p.groups = static_cast<int>((rows + per - 1) / per);
   if (d == 128)
     return adjacent ? launch_rope_u<128, true, kPaged>(p, per, st) : launch_rope_u<128, false, kPaged>(p, per, st);
@@ -229,11 +232,11 @@ int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* inde
   p.status = status_ptr();
   if (!p.status) return MALA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // CTAs per row of masses: as many as keep all rows on the GPU at once, but
-  // no more than leave each 2K masses
+  // CTAs per row of masses: as many as keep all rows on the GPU at once (two
+  // CTAs to an SM), but no more than leave each 2K masses
   const long long rows = static_cast<long long>(B) * Hkv;
   int cluster = 1;
-  while (cluster < 8 && rows * cluster * 2 <= sm_count() && ld_mass > 2048 * cluster) cluster *= 2;
+  while (cluster < 8 && rows * cluster <= sm_count() && ld_mass > 2048 * cluster) cluster *= 2;
   switch (cluster) {
     case 1: return launch_select<1>(p, st);
     case 2: return launch_select<2>(p, st);

@@ -57,6 +57,7 @@ struct KeyMassParams {
   const int* cu_k;
   int total_q, total_k;
   float scale_log2, decay;
+  float lse_hi, lse_lo;  // log2(e) as the rounded scale_log2 has it, in two parts (neg_lse2)
   const float* mass_in;  // [B, Hkv, ld], nullable
   float* mass_out;
   int ld;
@@ -116,6 +117,13 @@ __device__ __forceinline__ KeyMassSeq key_mass_seq(const KeyMassParams& p, int b
 // the first query tile with a row that sees key k0
 __device__ __forceinline__ int key_mass_qt0(const KeyMassSeq& s, int k0) {
   return max(0, k0 - s.P0 - s.first) / 128;
+}
+
+// -LSE in the units of the scores: times the log2(e) that the rounded scale_log2
+// applies to them, not one rounded on its own (the difference, up to 6e-8 of a
+// score of 20, would be an error of every weight).
+__device__ __forceinline__ float neg_lse2(const KeyMassParams& p, float lse) {
+  return fabsf(lse) == INFINITY ? -lse : -fmaf(lse, p.lse_hi, lse * p.lse_lo);
 }
 
 // 2^x of a packed pair on the FMA pipes: x = n + f with n the nearest integer,
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
       }
       issued = n + 1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sLse[st * 128 + e * 32 + lane] = cur[e] * -1.4426950408889634f;
+      for (int e = 0; e < 4; ++e) sLse[st * 128 + e * 32 + lane] = neg_lse2(p, cur[e]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[st]);
 #pragma unroll

@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
     float l = -INFINITY;
     if (g < p.G && r < rows) {
       const int hq = hkv * p.G + g;
-      l = -1.4426950408889634f * __ldg(p.cu_q != nullptr ? p.lse + static_cast<size_t>(hq) * p.total_q + sq.q_off + i
-                                                         : p.lse + (static_cast<size_t>(b) * p.Hq + hq) * sq.Lq + i);
+      l = neg_lse2(p, __ldg(p.cu_q != nullptr ? p.lse + static_cast<size_t>(hq) * p.total_q + sq.q_off + i
+                                              : p.lse + (static_cast<size_t>(b) * p.Hq + hq) * sq.Lq + i));
     }
     sLse[c] = l;
     sPos[c] = sq.P0 + i;
