@@ -506,12 +506,14 @@ MALA_API int mala_key_mass_varlen(const void* q, const void* k, const float* lse
              int ld_mass, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Workspace bytes mala_decode_paged_mass needs: fp32 scores [B, Hkv,
- * max_pages_per_seq * page_size, Hq / Hkv] and the split partials of
- * mala_decode_workspace_size, each 256-byte aligned. 0 for invalid sizes.
+ * Workspace bytes mala_decode_paged_mass needs: fp32 scores [B, Hkv, Hq / Hkv,
+ * max_pages_per_seq * page_size] and partial results (O, LSE), each 256-byte
+ * aligned. n_splits: the count used if tau > 0 (as in
+ * mala_decode_workspace_size), 0 for tau = 0. 0 for invalid sizes. Depends on
+ * its arguments and the current device's SM count.
  */
-MALA_API size_t mala_decode_mass_workspace_size(int B, int Hq, int d, int page_size, int max_pages_per_seq,
-             int n_splits);
+MALA_API size_t mala_decode_mass_workspace_size(int B, int Hq, int Hkv, int d, int page_size,
+             int max_pages_per_seq, int n_splits);
 
 /*
  * mala_decode_paged_mass -- mala_decode_paged that also collects each key's
@@ -519,9 +521,11 @@ MALA_API size_t mala_decode_mass_workspace_size(int B, int Hq, int d, int page_s
  *
  *     mass_out[b, hkv, j] = decay * mass_in[b, hkv, j] + sum over heads h of the group of exp(s_hj - LSE_h)
  *
- * O, LSE, kept_tiles and keep_map are those of mala_decode_paged. The newest key
- * (j = seqlens_k[b] - 1) is the query's own and starts from 0. A sequence of
- * length 0 is an idle slot: O = 0, LSE = -infinity, masses 0, no error.
+ * O, LSE, kept_tiles and keep_map are those of mala_decode_paged (with tau = 0 up
+ * to rounding: nothing is gated then, n_splits is not looked at, and the tiles of
+ * all sequences are dealt evenly over the GPU). The newest key (j = seqlens_k[b]
+ * - 1) is the query's own and starts from 0. A sequence of length 0 is an idle
+ * slot: O = 0, LSE = -infinity, masses 0, no error.
  *
  *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
  *   mass_out   [B, Hkv, ld_mass] fp32, out; entries past a sequence's keys

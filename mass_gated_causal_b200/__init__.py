@@ -108,7 +108,7 @@ _lib.mala_key_mass.argtypes = [_vp] * 5 + [_i] * 6 + [_f, _i, _f, _i, _vp, _sz, 
 _lib.mala_key_mass.restype = _i
 _lib.mala_key_mass_varlen.argtypes = [_vp] * 7 + [_i] * 8 + [_f, _i, _f, _i, _vp, _sz, _vp]
 _lib.mala_key_mass_varlen.restype = _i
-_lib.mala_decode_mass_workspace_size.argtypes = [_i] * 6
+_lib.mala_decode_mass_workspace_size.argtypes = [_i] * 7
 _lib.mala_decode_mass_workspace_size.restype = _sz
 _lib.mala_decode_paged_mass.argtypes = [_vp] * 9 + [_i] * 7 + [_f, _f, _f, _i, _i, _vp, _sz, _vp, _vp, _vp]
 _lib.mala_decode_paged_mass.restype = _i
@@ -308,8 +308,8 @@ def mala_key_mass_varlen(q, k, lse, cu_seqlens_q, cu_seqlens_k, mass_in, mass_ou
                                          int(workspace_bytes), _stream(stream)))
 
 
-def mala_decode_mass_workspace_size(B, Hq, d, page_size, max_pages_per_seq, n_splits) -> int:
-    return int(_lib.mala_decode_mass_workspace_size(B, Hq, d, page_size, max_pages_per_seq, n_splits))
+def mala_decode_mass_workspace_size(B, Hq, Hkv, d, page_size, max_pages_per_seq, n_splits) -> int:
+    return int(_lib.mala_decode_mass_workspace_size(B, Hq, Hkv, d, page_size, max_pages_per_seq, n_splits))
 
 
 def mala_decode_paged_mass(q, k_pages, v_pages, block_table, seqlens_k, o, lse, mass_in, mass_out, B, Hq, Hkv,
@@ -588,7 +588,8 @@ def decode_paged_mass(q, k_pages, v_pages, block_table, seqlens_k, scale: float,
                       decay: float = 1.0, out=None, n_splits: int = 0, keep_map: bool = False, workspace=None,
                       stream=None):
     """decode_paged that also collects each key's weight: mass [B,Hkv,ld] fp32 of earlier calls (None: 0), ld >=
-    max_pages * page -> (o, lse, kept_tiles, keep_map|None, n_splits, mass); out: where the masses go (may be mass)."""
+    max_pages * page -> (o, lse, kept_tiles, keep_map|None, n_splits (0 without a gate), mass); out: where the masses
+    go (may be mass)."""
     return (_native or _load_native()).decode_paged_mass(q, k_pages, v_pages, block_table, seqlens_k, scale, tau, mass,
                                                          decay, out, n_splits, keep_map, workspace, stream)
 

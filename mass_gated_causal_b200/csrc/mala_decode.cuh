@@ -65,7 +65,7 @@ struct DecParams {
   unsigned* status;
   uint64_t wait_ns;  // limit of each bounded wait
   int stall_tile;    // test hook (-1: off): the K producer stalls before this tile
-  float* scores;     // kScores: [B, Hkv, max_pages * Bk, G] scores in log2 units (live keys only)
+  float* scores;     // kScores: [B, Hkv, G, max_pages * Bk] scores in log2 units (live keys only)
 };
 
 // Sum N per-lane values over the L lanes of a group (lane index c = lane % L,
@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(320, 1)
 
   auto row_addr = [&](uint32_t base, int j) { return base + chunk_atom + j * 128 + ((chunk_in ^ (j & 7)) << 4); };
 
-  // kScores: this (b, KV head)'s scores, G to a key
-  float* score_row = kScores ? p.scores + static_cast<size_t>(b * p.Hkv + hkv) * p.max_pages * BK * G : nullptr;
+  // kScores: this (b, KV head)'s scores, a row per head of the group
+  const size_t score_ld = kScores ? static_cast<size_t>(p.max_pages) * BK : 0;
+  float* score_row = kScores ? p.scores + static_cast<size_t>(b * p.Hkv + hkv) * G * score_ld : nullptr;
   // paged: rows of the split's newest tile (always its first kept one) that hold keys. The rest
   // of its page is whatever the pool held, perhaps not finite, and 0 times that is not 0.
   const int live0 = kPaged ? Lk - (t1 - 1) * BK : BK;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(320, 1)
       for (int i = 0; i < VPL; ++i) {
         sc[i] = live ? part[i] : -INFINITY;
         mx[i] = sc[i];
-        if (kScores && live && g0 + i < G) score_row[static_cast<size_t>(kb * BK + j) * G + g0 + i] = part[i] * c2;
+        if (kScores && live && g0 + i < G) score_row[(g0 + i) * score_ld + kb * BK + j] = part[i] * c2;
       }
       // max over the warp's keys: the other steps' lanes, then the other key groups
 #pragma unroll
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(320, 1)
         if (live) mx = fmaxf(mx, mine);
         sc[s2] = live ? mine : -INFINITY;
         if (kScores && live && hh < G && (c % LPH) == 0)
-          score_row[static_cast<size_t>(kb * BK + j) * G + hh] = mine * c2;
+          score_row[hh * score_ld + kb * BK + j] = mine * c2;
       }
       mbar_arrive(&k_empty[st]);  // my reads of this K stage are done
 #pragma unroll

@@ -1,8 +1,9 @@
 // mala_decode_mass.cuh -- the second kernel of a decode that also collects
 // each key's attention weight.
 //
-// The split kernel (mala_decode.cuh, kScores) has written every live key's
-// scores and the splits' (O_s, LSE_s). What is left is, per (b, query head),
+// The first kernel (mala_decode.cuh with kScores behind a gate, else
+// mala_decode_flat.cuh) has written every live key's scores and partial results
+// (O_s, LSE_s). What is left is, per (b, query head),
 //   LSE = log sum_s exp(LSE_s),   O = sum_s exp(LSE_s - LSE) O_s,
 // and per (b, KV head, key j), over the group's query heads h,
 //   mass_j = decay * mass_j' + sum_h exp(s_hj - LSE_h),
@@ -10,42 +11,60 @@
 // kept or skipped, so the weights cost no second pass over K: G scores (4 G
 // bytes) are written and read per key and KV head, against 4 d bytes of K and V.
 //
-// One launch does both: the first blocks merge the splits, a warp per (b,
+// One launch does both: the first blocks merge the partials, a warp per (b,
 // query head); the others take 1024 keys of one (b, KV head) each and form the
-// LSEs of its G heads from the partials again (G x n_splits values, from L2),
-// so they wait for nothing.
+// LSEs of its G heads from the partials again (a few dozen values a head, from
+// L2), so they wait for nothing but the first kernel.
 #pragma once
 
-#include "mala_ptx.cuh"
+#include "mala_decode_flat.cuh"
 
 namespace mala {
 
 struct DecMassParams {
-  const float* o_part;    // [B, Hq, S, d]
-  const float* lse_part;  // [B, Hq, S]
+  const float* o_part;    // [B, Hq, slots, d]
+  const float* lse_part;  // [B, Hq, slots]
   uint16_t* o;            // [B, Hq, d]
   float* lse;             // [B, Hq]
-  const float* scores;    // [B, Hkv, ld_scores, G], log2 units
+  const float* scores;    // [B, Hkv, G, max_len], log2 units
   const int32_t* seqlens;
   const float* mass_in;   // [B, Hkv, ld], nullable
   float* mass_out;
-  int B, Hq, Hkv, G, n_splits, ld, ld_scores, max_len;
+  const int* plan;        // mala_decode_flat_kernel's (null: every unit has `slots` partials)
+  int32_t* kept_tiles;    // with a plan: written here (every tile is kept)
+  uint8_t* keep_map;
+  int B, Hq, Hkv, G, slots, ld, max_len, max_pages, page;
   int merge_blocks, key_blocks;  // blocks of the merge; blocks per (b, KV head)
   float decay;
 };
 
 constexpr int kDecMassThreads = 256;
-constexpr int kDecMassKeys = 1024;  // keys per block
+constexpr int kDecMassKeys = 1024;  // keys per block, four consecutive ones to a thread
 
-// log sum exp over the splits of one row, by a warp (every lane returns it)
-__device__ __forceinline__ float merged_lse(const float* lp, int n_splits, int lane) {
+// length of sequence b (0: idle, or invalid and reported by the first kernel)
+__device__ __forceinline__ int mass_len(const DecMassParams& p, int b) {
+  const int L = __ldg(p.seqlens + b);
+  return L < 0 || L > p.max_len ? 0 : L;
+}
+
+// partial results of (b, KV head)
+__device__ __forceinline__ int mass_parts(const DecMassParams& p, int b, int hkv, int len) {
+  if (p.plan == nullptr) return p.slots;
+  const int nt = (len + kFlatTile - 1) / kFlatTile, run = p.plan[p.B];
+  if (nt == 0) return 0;
+  const int at = p.plan[b] + hkv * nt;
+  return (at + nt - 1) / run - at / run + 1;
+}
+
+// log sum exp of n values, by a warp (every lane returns it)
+__device__ __forceinline__ float merged_lse(const float* lp, int n, int lane) {
   float mx = -INFINITY;
-  for (int s = lane; s < n_splits; s += 32) mx = fmaxf(mx, __ldg(lp + s));
+  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, lp[s]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float z = 0.f;
-  for (int s = lane; s < n_splits; s += 32) {
-    const float x = __ldg(lp + s);
+  for (int s = lane; s < n; s += 32) {
+    const float x = lp[s];
     z += x == -INFINITY ? 0.f : __expf(x - mx);
   }
 #pragma unroll
@@ -56,61 +75,87 @@ __device__ __forceinline__ float merged_lse(const float* lp, int n_splits, int l
 template <int D>
 __global__ void __launch_bounds__(kDecMassThreads) mala_decode_mass_kernel(const DecMassParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_wait();
   if (static_cast<int>(blockIdx.x) < p.merge_blocks) {
     const int row = blockIdx.x * (kDecMassThreads / 32) + warp;
     if (row >= p.B * p.Hq) return;
-    const float* lp = p.lse_part + static_cast<size_t>(row) * p.n_splits;
-    const float L = merged_lse(lp, p.n_splits, lane);
+    const int b = row / p.Hq, len = mass_len(p, b);
+    const int n = mass_parts(p, b, row % p.Hq / p.G, len);
+    const float* lp = p.lse_part + static_cast<size_t>(row) * p.slots;
+    const float L = merged_lse(lp, n, lane);
     constexpr int PER = D / 32;
     float out[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) out[e] = 0.f;
-    for (int s = 0; s < p.n_splits; ++s) {
-      const float ls = __ldg(lp + s);
-      if (ls == -INFINITY) continue;
-      const float w = __expf(ls - L);
-      const float* src = p.o_part + (static_cast<size_t>(row) * p.n_splits + s) * D + lane * PER;
+    const float* src = p.o_part + static_cast<size_t>(row) * p.slots * D + lane * PER;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float ls = lp[s];
+      const float w = ls == -INFINITY ? 0.f : __expf(ls - L);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) out[e] = fmaf(w, src[e], out[e]);
+      for (int e = 0; e < PER; ++e) out[e] = fmaf(w, src[static_cast<size_t>(s) * D + e], out[e]);
     }
 #pragma unroll
     for (int e = 0; e < PER; e += 2)
       *reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(row) * D + lane * PER + e) =
           pack_bf16x2(out[e], out[e + 1]);
     if (lane == 0) p.lse[row] = L;
+    if (p.plan != nullptr) {
+      const int pages = (len + p.page - 1) / p.page;
+      if (lane == 0) p.kept_tiles[row] = pages;
+      if (p.keep_map != nullptr)
+        for (int i = lane; i < pages; i += 32) p.keep_map[static_cast<size_t>(row) * p.max_pages + i] = 1;
+    }
     return;
   }
 
   const int blk = blockIdx.x - p.merge_blocks;
-  const int bk = blk / p.key_blocks, j0 = (blk % p.key_blocks) * kDecMassKeys;
+  const int bk = blk / p.key_blocks;
   const int b = bk / p.Hkv, hkv = bk % p.Hkv;
-  int L = __ldg(p.seqlens + b);
-  if (L < 0 || L > p.max_len) L = 0;  // reported by the split kernel; the sequence has no weights
-  const float* min = p.mass_in ? p.mass_in + static_cast<size_t>(bk) * p.ld : nullptr;
-  float* mout = p.mass_out + static_cast<size_t>(bk) * p.ld;
-  const int j1 = ::min(j0 + kDecMassKeys, p.ld);
+  const int L = mass_len(p, b);
+  const int j0 = (blk % p.key_blocks) * kDecMassKeys;
   __shared__ float lse2[8];
   if (j0 < L && warp < p.G) {
-    const float x = merged_lse(p.lse_part + (static_cast<size_t>(b) * p.Hq + hkv * p.G + warp) * p.n_splits,
-                               p.n_splits, lane);
+    const float x = merged_lse(p.lse_part + (static_cast<size_t>(b) * p.Hq + hkv * p.G + warp) * p.slots,
+                               mass_parts(p, b, hkv, L), lane);
     if (lane == 0) lse2[warp] = x * 1.4426950408889634f;
   }
   __syncthreads();
-  const float* sc = p.scores + static_cast<size_t>(bk) * p.ld_scores * p.G;
-  for (int j = j0 + static_cast<int>(threadIdx.x); j < j1; j += kDecMassThreads) {
-    float m = 0.f;
-    if (j < L) {
-      const float* s = sc + static_cast<size_t>(j) * p.G;
-      if (p.G == 4) {  // one 16-byte load
-        const float4 x = *reinterpret_cast<const float4*>(s);
-        m = (ex2_approx(x.x - lse2[0]) + ex2_approx(x.y - lse2[1])) +
-            (ex2_approx(x.z - lse2[2]) + ex2_approx(x.w - lse2[3]));
-      } else {
-        for (int g = 0; g < p.G; ++g) m += ex2_approx(s[g] - lse2[g]);
-      }
-      if (min != nullptr && p.decay != 0.f && j < L - 1) m = fmaf(p.decay, min[j], m);
+  const int j = j0 + 4 * static_cast<int>(threadIdx.x);
+  if (j >= p.ld) return;
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+  if (j < L) {
+    const float* sc = p.scores + static_cast<size_t>(bk) * p.G * p.max_len + j;
+    for (int g = 0; g < p.G; ++g) {
+      const float4 x = *reinterpret_cast<const float4*>(sc + static_cast<size_t>(g) * p.max_len);
+      const float l2 = lse2[g];
+      m[0] += ex2_approx(x.x - l2);
+      m[1] += ex2_approx(x.y - l2);
+      m[2] += ex2_approx(x.z - l2);
+      m[3] += ex2_approx(x.w - l2);
     }
-    mout[j] = m;  // past the sequence's keys: 0
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e >= L) m[e] = 0.f;  // past the sequence's keys
+  }
+  const size_t at = static_cast<size_t>(bk) * p.ld + j;
+  const bool old = p.mass_in != nullptr && p.decay != 0.f && j < L - 1;
+  if ((p.ld & 3) == 0) {  // whole 16-byte words
+    if (old) {
+      const float4 x = *reinterpret_cast<const float4*>(p.mass_in + at);
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < L - 1) m[e] = fmaf(p.decay, v[e], m[e]);
+    }
+    *reinterpret_cast<float4*>(p.mass_out + at) = make_float4(m[0], m[1], m[2], m[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (j + e >= p.ld) break;
+      if (old && j + e < L - 1) m[e] = fmaf(p.decay, p.mass_in[at + e], m[e]);
+      p.mass_out[at + e] = m[e];
+    }
   }
 }
 

@@ -11,50 +11,67 @@ using namespace mala::host;
 namespace {
 
 struct Layout {
-  size_t scores, o_part, lse_part, total;
+  size_t scores, o_part, lse_part, plan, total;
+  int slots;  // partial results of a (b, query head)
 };
 
-Layout layout(int B, int Hq, long long keys, int d, int n_splits) {
+// CTAs of the ungated kernel: two to an SM.
+int flat_grid() { return 2 * sm_count(); }
+
+// n_splits > 0: the gated kernel's partials; 0: the ungated kernel's. Its runs are at
+// least kFlatLeastRun tiles and at least an even share of all tiles, of which one
+// (b, KV head) holds at most a 1 / Hkv part, so it meets at most that many runs.
+Layout layout(int B, int Hq, int Hkv, long long keys, int d, int n_splits) {
   Layout w;
+  const long long tiles = (keys + mala::kFlatTile - 1) / mala::kFlatTile;
+  const long long shared = (flat_grid() + Hkv - 1) / Hkv;
+  w.slots = n_splits > 0 ? n_splits
+                         : static_cast<int>(std::min((tiles + mala::kFlatLeastRun - 1) / mala::kFlatLeastRun, shared)) + 1;
   const size_t rows = static_cast<size_t>(B) * Hq;
   w.scores = 0;
   w.o_part = align256(rows * keys * 4);
-  w.lse_part = w.o_part + align256(rows * n_splits * d * 4);
-  w.total = w.lse_part + align256(rows * n_splits * 4);
+  w.lse_part = w.o_part + align256(rows * w.slots * d * 4);
+  w.plan = w.lse_part + align256(rows * w.slots * 4);
+  w.total = w.plan + align256((static_cast<size_t>(B) + 1) * 4);
   return w;
 }
 
-template <int D, int BK, int GP, bool G>
+template <int D>
+int launch_flat(const CUtensorMap& mk, const CUtensorMap& mv, const mala::FlatParams& p, cudaStream_t st) {
+  using Lay = mala::FlatLayout<D>;
+  auto kern = mala::mala_decode_flat_kernel<D>;
+  if (set_smem(kern, Lay::ALLOC_BYTES) != MALA_OK) return MALA_ERR_CUDA;
+  kern<<<flat_grid(), mala::kFlatThreads, Lay::ALLOC_BYTES, st>>>(mk, mv, p);
+  return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
+}
+
+template <int D, int BK, int GP>
 int launch(const CUtensorMap& mk, const CUtensorMap& mv, const mala::DecParams& p, cudaStream_t st) {
   using Lay = mala::DecLayout<D, BK, GP>;
-  auto kern = mala::mala_decode_split_kernel<D, BK, GP, G, true, true>;
+  auto kern = mala::mala_decode_split_kernel<D, BK, GP, true, true, true>;
   if (set_smem(kern, Lay::ALLOC_BYTES) != MALA_OK) return MALA_ERR_CUDA;
   kern<<<static_cast<unsigned>(p.B) * p.Hkv * p.n_splits, 320, Lay::ALLOC_BYTES, st>>>(mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
 }
 
-template <int D, int BK, bool G>
-int launch_g(const CUtensorMap& mk, const CUtensorMap& mv, const mala::DecParams& p, cudaStream_t st) {
-  if (p.G <= 1) return launch<D, BK, 1, G>(mk, mv, p, st);
-  if (p.G <= 2) return launch<D, BK, 2, G>(mk, mv, p, st);
-  if (p.G <= 4) return launch<D, BK, 4, G>(mk, mv, p, st);
-  return launch<D, BK, 8, G>(mk, mv, p, st);
-}
-
 template <int D, int BK>
-int launch_gate(bool gate, const CUtensorMap& mk, const CUtensorMap& mv, const mala::DecParams& p, cudaStream_t st) {
-  return gate ? launch_g<D, BK, true>(mk, mv, p, st) : launch_g<D, BK, false>(mk, mv, p, st);
+int launch_g(const CUtensorMap& mk, const CUtensorMap& mv, const mala::DecParams& p, cudaStream_t st) {
+  if (p.G <= 1) return launch<D, BK, 1>(mk, mv, p, st);
+  if (p.G <= 2) return launch<D, BK, 2>(mk, mv, p, st);
+  if (p.G <= 4) return launch<D, BK, 4>(mk, mv, p, st);
+  return launch<D, BK, 8>(mk, mv, p, st);
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t mala_decode_mass_workspace_size(int B, int Hq, int d, int page_size, int max_pages_per_seq, int n_splits) {
-  if (B < 1 || Hq < 1 || max_pages_per_seq < 1 || n_splits < 1 || (d != 64 && d != 128) ||
+size_t mala_decode_mass_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq,
+                                       int n_splits) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || max_pages_per_seq < 1 || n_splits < 0 || (d != 64 && d != 128) ||
       (page_size != 64 && page_size != 128))
     return 0;
-  return layout(B, Hq, static_cast<long long>(max_pages_per_seq) * page_size, d, n_splits).total;
+  return layout(B, Hq, Hkv, static_cast<long long>(max_pages_per_seq) * page_size, d, n_splits).total;
 }
 
 int mala_decode_paged_mass(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
@@ -74,73 +91,106 @@ int mala_decode_paged_mass(const void* q, const void* k_pages, const void* v_pag
   if (!(decay >= 0.f) || !std::isfinite(decay) || ld_mass < Lk) return MALA_ERR_INVALID_ARG;
   if (!aligned16(mass_out) || (mass_in && !aligned16(mass_in))) return MALA_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_pages) * page_size * Hkv * d >= (1ll << 40)) return MALA_ERR_UNSUPPORTED;
-  if (n_splits == 0) n_splits = mala_decode_default_splits(B, Hkv, Lk, page_size);
+  // without a gate the tiles are dealt evenly over the GPU, whatever n_splits says
+  const bool gate = tau > 0.f;
+  if (!gate) n_splits = 0;
+  else if (n_splits == 0) n_splits = mala_decode_default_splits(B, Hkv, Lk, page_size);
   if (n_splits > 65535) return MALA_ERR_UNSUPPORTED;
-  const Layout lay = layout(B, Hq, max_lk, d, n_splits);
+  if (B * (max_lk / mala::kFlatTile) * Hkv >= (1ll << 31)) return MALA_ERR_UNSUPPORTED;
+  const Layout lay = layout(B, Hq, Hkv, max_lk, d, n_splits);
   if (!workspace || workspace_bytes < lay.total || !aligned256(workspace)) return MALA_ERR_WORKSPACE;
   const int key_blocks = (ld_mass + mala::kDecMassKeys - 1) / mala::kDecMassKeys;
   const int merge_blocks = (B * Hq + mala::kDecMassThreads / 32 - 1) / (mala::kDecMassThreads / 32);
   const long long blocks = merge_blocks + static_cast<long long>(B) * Hkv * key_blocks;
   if (blocks >= (1ll << 31) || static_cast<long long>(B) * Hkv * n_splits >= (1ll << 31)) return MALA_ERR_UNSUPPORTED;
+  const int rows = gate ? page_size : mala::kFlatTile;
   CUtensorMap mk, mv;
-  if (!make_bshd_map(&mk, k_pages, num_pages, page_size, Hkv, d, page_size) ||
-      !make_bshd_map(&mv, v_pages, num_pages, page_size, Hkv, d, page_size))
+  if (!make_bshd_map(&mk, k_pages, num_pages, page_size, Hkv, d, rows) ||
+      !make_bshd_map(&mv, v_pages, num_pages, page_size, Hkv, d, rows))
     return MALA_ERR_CUDA;
   unsigned* status = status_ptr();
   if (!status) return MALA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
 
-  mala::DecParams p = {};
-  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Lk = Lk; p.G = Hq / Hkv;
-  p.nk = max_pages_per_seq;
-  p.n_splits = n_splits;
-  p.tiles_per_split = (p.nk + n_splits - 1) / n_splits;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.log2_tau = tau > 0.f ? std::log2(tau) : 0.f;
-  p.seqlens = seqlens_k;
-  p.block_table = block_table;
-  p.max_pages = max_pages_per_seq;
-  p.num_pages = num_pages;
-  p.q = static_cast<const uint16_t*>(q);
-  p.o_part = reinterpret_cast<float*>(ws + lay.o_part);
-  p.lse_part = reinterpret_cast<float*>(ws + lay.lse_part);
-  p.kept_tiles = kept_tiles;
-  p.keep_map = keep_map;
-  p.status = status;
-  p.wait_ns = wait_limit_ns();
-  p.stall_tile = stall_tile();
-  p.scores = reinterpret_cast<float*>(ws + lay.scores);
-  if (cudaMemsetAsync(kept_tiles, 0, sizeof(int32_t) * B * Hq, st) != cudaSuccess) return MALA_ERR_CUDA;
-  const bool gate = tau > 0.f;
-  if (d == 128 && page_size == 128) rc = launch_gate<128, 128>(gate, mk, mv, p, st);
-  else if (d == 64 && page_size == 128) rc = launch_gate<64, 128>(gate, mk, mv, p, st);
-  else if (d == 128) rc = launch_gate<128, 64>(gate, mk, mv, p, st);
-  else rc = launch_gate<64, 64>(gate, mk, mv, p, st);
+  float* scores = reinterpret_cast<float*>(ws + lay.scores);
+  float* o_part = reinterpret_cast<float*>(ws + lay.o_part);
+  float* lse_part = reinterpret_cast<float*>(ws + lay.lse_part);
+  int* plan = reinterpret_cast<int*>(ws + lay.plan);
+  const int G = Hq / Hkv;
+  if (gate) {
+    mala::DecParams p = {};
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Lk = Lk; p.G = G;
+    p.nk = max_pages_per_seq;
+    p.n_splits = n_splits;
+    p.tiles_per_split = (p.nk + n_splits - 1) / n_splits;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.log2_tau = std::log2(tau);
+    p.seqlens = seqlens_k;
+    p.block_table = block_table;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.q = static_cast<const uint16_t*>(q);
+    p.o_part = o_part;
+    p.lse_part = lse_part;
+    p.kept_tiles = kept_tiles;
+    p.keep_map = keep_map;
+    p.status = status;
+    p.wait_ns = wait_limit_ns();
+    p.stall_tile = stall_tile();
+    p.scores = scores;
+    if (cudaMemsetAsync(kept_tiles, 0, sizeof(int32_t) * B * Hq, st) != cudaSuccess) return MALA_ERR_CUDA;
+    if (d == 128 && page_size == 128) rc = launch_g<128, 128>(mk, mv, p, st);
+    else if (d == 64 && page_size == 128) rc = launch_g<64, 128>(mk, mv, p, st);
+    else if (d == 128) rc = launch_g<128, 64>(mk, mv, p, st);
+    else rc = launch_g<64, 64>(mk, mv, p, st);
+  } else {
+    mala::FlatParams p = {};
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = G;
+    p.seqlens = seqlens_k;
+    p.block_table = block_table;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.page_shift = page_size == 64 ? 6 : 7;
+    p.max_len = Lk;
+    p.q = static_cast<const uint16_t*>(q);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.o_part = o_part;
+    p.lse_part = lse_part;
+    p.scores = scores;
+    p.plan = plan;
+    p.slots = lay.slots;
+    p.status = status;
+    p.wait_ns = wait_limit_ns();
+    p.stall_tile = stall_tile();
+    rc = d == 128 ? launch_flat<128>(mk, mv, p, st) : launch_flat<64>(mk, mv, p, st);
+  }
   if (rc != MALA_OK) return rc;
 
   mala::DecMassParams m = {};
-  m.o_part = p.o_part;
-  m.lse_part = p.lse_part;
+  m.o_part = o_part;
+  m.lse_part = lse_part;
   m.o = static_cast<uint16_t*>(o);
   m.lse = lse;
-  m.scores = p.scores;
+  m.scores = scores;
   m.seqlens = seqlens_k;
   m.mass_in = mass_in;
   m.mass_out = mass_out;
-  m.B = B; m.Hq = Hq; m.Hkv = Hkv; m.G = p.G;
-  m.n_splits = n_splits;
+  m.plan = gate ? nullptr : plan;
+  m.kept_tiles = kept_tiles;
+  m.keep_map = keep_map;
+  m.B = B; m.Hq = Hq; m.Hkv = Hkv; m.G = G;
+  m.slots = lay.slots;
   m.ld = ld_mass;
-  m.ld_scores = Lk;
   m.max_len = Lk;
+  m.max_pages = max_pages_per_seq;
+  m.page = page_size;
   m.merge_blocks = merge_blocks;
   m.key_blocks = key_blocks;
   m.decay = decay;
-  if (d == 128)
-    mala::mala_decode_mass_kernel<128><<<static_cast<unsigned>(blocks), mala::kDecMassThreads, 0, st>>>(m);
-  else
-    mala::mala_decode_mass_kernel<64><<<static_cast<unsigned>(blocks), mala::kDecMassThreads, 0, st>>>(m);
-  return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
+  // its launch overlaps the first kernel's end; it waits for that kernel itself
+  auto kern = d == 128 ? mala::mala_decode_mass_kernel<128> : mala::mala_decode_mass_kernel<64>;
+  return launch_dependent(kern, static_cast<unsigned>(blocks), mala::kDecMassThreads, st, m);
 }
 
 }  // extern "C"

@@ -312,7 +312,8 @@ std::tuple<Tensor, Tensor, Tensor, OptTensor, int, Tensor> decode_paged_mass(
   const Tensor to = mass_out(place, mass, out, B, Hkv, maxp * page);
   const int b = c_int(where, B), hq = c_int(where, Hq), hkv = c_int(where, Hkv), di = c_int(where, d),
             pg = c_int(where, page), mp = c_int(where, maxp);
-  if (n_splits == 0) n_splits = mala_decode_default_splits(b, hkv, c_int(where, maxp * page), pg);
+  if (!(tau > 0)) n_splits = 0;  // nothing is split by count
+  else if (n_splits == 0) n_splits = mala_decode_default_splits(b, hkv, c_int(where, maxp * page), pg);
   const Tensor o = place.empty(q.sizes(), kBf16), lse = place.empty({B, Hq}, kF32), kept = place.empty({B * Hq}, kI32);
   OptTensor km;
   if (keep_map) {
@@ -322,7 +323,7 @@ std::tuple<Tensor, Tensor, Tensor, OptTensor, int, Tensor> decode_paged_mass(
   }
   Tensor hold;
   const auto ws =
-      place.scratch(workspace, workspace ? 0 : mala_decode_mass_workspace_size(b, hq, di, pg, mp, n_splits), hold);
+      place.scratch(workspace, workspace ? 0 : mala_decode_mass_workspace_size(b, hq, hkv, di, pg, mp, n_splits), hold);
   check(mala_decode_paged_mass(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), iptr(block_table), iptr(seqlens_k),
                                o.data_ptr(), fptr(lse), fptr(mass), fptr(to), b, hq, hkv, c_int(where, k_pages.size(0)),
                                pg, mp, di, static_cast<float>(scale), static_cast<float>(tau),

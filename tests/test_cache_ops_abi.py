@@ -140,8 +140,13 @@ def test_decode_paged_mass_rejects(kw, code):
 def test_decode_mass_workspace_size():
     a256 = lambda x: (x + 255) // 256 * 256
     ws = mala.mala_decode_mass_workspace_size
-    assert ws(4, 8, 128, 128, 40, 5) == a256(4 * 8 * 40 * 128 * 4) + mala.mala_decode_workspace_size(4, 8, 128, 5)
-    assert ws(4, 8, 96, 128, 40, 5) == 0 and ws(4, 8, 128, 100, 40, 5) == 0 and ws(4, 8, 128, 128, 40, 0) == 0
+    scores, plan = a256(4 * 8 * 40 * 128 * 4), a256(5 * 4)
+    # behind a gate: a partial for each split
+    assert ws(4, 8, 2, 128, 128, 40, 5) == scores + mala.mala_decode_workspace_size(4, 8, 128, 5) + plan
+    # without: 80 tiles in runs of at least two, and one run more that begins before them
+    assert ws(4, 8, 2, 128, 128, 40, 0) == scores + mala.mala_decode_workspace_size(4, 8, 128, 41) + plan
+    for bad in ((4, 8, 2, 96, 128, 40, 5), (4, 8, 2, 128, 100, 40, 5), (4, 8, 2, 128, 128, 40, -1), (4, 8, 0, 128, 128, 40, 5)):
+        assert ws(*bad) == 0
 
 
 def select(**kw):

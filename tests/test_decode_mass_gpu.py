@@ -1,11 +1,13 @@
-"""Paged decode that collects each key's weight (mala_decode_paged_mass): its
-attention equals mala_decode_paged bit for bit, and its masses equal weights
-formed in 64 bits from its own LSE.
+"""Paged decode that collects each key's weight (mala_decode_paged_mass): behind a
+gate its attention equals mala_decode_paged bit for bit; without one (another
+kernel) it is held to 64 bits; its masses equal weights formed in 64 bits from its
+own LSE.
 
 Tolerance of a weight, relative: the score is an fp32 sum of d products (d 2^-24
 scale sum_c |q_c k_c|), x = s log2e - LSE log2e rounds at its terms' size
 (3 x 2^-24 (|s| + |LSE|) log2e), exp2 is good to 2^-21, the sums of at most eight
-terms and the decayed mass to 8 x 2^-24.
+terms and the decayed mass to 8 x 2^-24. An output: rounded once to bf16 (2^-8 of
+its value at most, 2^-9 on average), from probabilities held to 16 bits.
 """
 import pytest
 import torch
@@ -48,6 +50,10 @@ CASES = [
     ([700, 20], 16, 2, 128, 128, 0.0, 4),
     ([2100], 3, 3, 128, 64, 1.0, 40),         # more splits than tiles
     ([900, 130], 10, 2, 128, 128, 1.0, 2),    # groups of five
+    ([64, 1, 700, 65, 64, 333, 2, 128] * 9, 8, 2, 128, 64, 0.0, 0),   # runs over many short sequences
+    ([40000, 17], 8, 1, 64, 128, 0.0, 0),     # and over a part of one long one
+    ([30001], 16, 2, 128, 128, 0.0, 0),
+    ([129, 4000], 5, 1, 64, 64, 0.0, 0),
 ]
 
 
@@ -64,7 +70,9 @@ def test_decode_paged_mass(cuda_lib, lens, Hq, Hkv, d, page, tau, n_splits):
                                                            n_splits=n_splits, keep_map=True)
     o2, lse2, kept2, km2, _ = cuda_lib.decode_paged(q, kp, vp, table, sl, scale, tau, n_splits=ns, keep_map=True)
     assert cuda_lib.mala_check_status() == 0
-    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(kept, kept2) and torch.equal(km, km2)
+    assert torch.equal(kept, kept2) and torch.equal(km, km2) and (ns > 0) == (tau > 0)
+    if tau > 0:
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
     alone = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, scale, tau, n_splits=n_splits)[-1]
     for b, n in enumerate(lens):
         k = gathered(kp, table[b], n)
@@ -75,10 +83,12 @@ def test_decode_paged_mass(cuda_lib, lens, Hq, Hkv, d, page, tau, n_splits):
         if tau == 0:  # the whole row's weights, and the output, from 64 bits
             v = gathered(vp, table[b], n).double()
             s = torch.einsum("hgd,nhd->hgn", q[b].double().view(Hkv, -1, d), k.double()) * scale
-            assert float((torch.logsumexp(s, -1).view(-1) - lse[b].double()).abs().max()) <= 1e-4
+            assert float((torch.logsumexp(s, -1).view(-1) - lse[b].double()).abs().max()) <= rel
             p = torch.softmax(s, -1)
             want_o = torch.einsum("hgn,nhd->hgd", p, v).view(Hq, d)
-            assert float((o[b].double() - want_o).norm() / want_o.norm()) <= 4e-3
+            size = torch.einsum("hgn,nhd->hgd", p, v.abs()).view(Hq, d)
+            err = (o[b].double() - want_o).abs()
+            assert bool((err <= 2.0 ** -8 * want_o.abs() + (2.0 ** -16 + 2 * rel) * size).all())
 
 
 def test_in_place_and_not_read(cuda_lib):
@@ -119,7 +129,10 @@ def test_what_lies_behind_the_keys_does_not_count(cuda_lib, d, page, G):
     # the same tails under the plain paged decode (which has no idle slots)
     o = cuda_lib.decode_paged(q[[0, 2, 3]].contiguous(), kp, vp, table[[0, 2, 3]].contiguous(),
                               sl[[0, 2, 3]].contiguous(), 0.1, 0.0, n_splits=2)[0]
-    assert torch.equal(o, got[0][[0, 2, 3]])
+    assert bool(torch.isfinite(o.float()).all())
+    # two kernels: each within half a bf16 step and the sums' rounding of the same value
+    same = got[0][[0, 2, 3]].float()
+    assert bool(((o.float() - same).abs() <= 2.0 ** -7 * same.abs() + 1e-4 * float(same.abs().max())).all())
 
 
 def test_bad_tables_are_reported(cuda_lib):
@@ -143,18 +156,22 @@ def test_bad_tables_are_reported(cuda_lib):
     assert cuda_lib.mala_check_status() == 0
 
 
-def test_a_wait_that_runs_out_is_reported(cuda_lib):
+@pytest.mark.parametrize("tau,tile,reached", [
+    (1.0, 2, True), (0.0, 1, True), (0.0, 0, True),
+    (0.0, 2, False),  # twenty tiles in runs of two: no run has a tile 2
+])
+def test_a_wait_that_runs_out_is_reported(cuda_lib, tau, tile, reached):
     kp, vp, table = paged(1, 600, 2, 64, 64, seed=9)
     q = torch.randn(1, 4, 64, device="cuda").to(torch.bfloat16)
     sl = torch.tensor([600], dtype=torch.int32, device="cuda")
-    want = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.125, 0.0, n_splits=1)
-    cuda_lib.mala_test_hooks(20_000_000, 2, None)
+    want = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.125, tau, n_splits=1)
+    cuda_lib.mala_test_hooks(20_000_000, tile, None)
     try:
-        cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.125, 0.0, n_splits=1)
-        assert cuda_lib.mala_check_status() == cuda_lib.MALA_ERR_DEVICE_TIMEOUT
+        cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.125, tau, n_splits=1)
+        assert cuda_lib.mala_check_status() == (cuda_lib.MALA_ERR_DEVICE_TIMEOUT if reached else 0)
     finally:
         cuda_lib.mala_test_hooks(0, -1, None)
-    got = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.125, 0.0, n_splits=1)
+    got = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.125, tau, n_splits=1)
     assert cuda_lib.mala_check_status() == 0
     assert torch.equal(got[5], want[5])
 
