@@ -82,10 +82,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// the next kernel of the stream may start; it waits for this one with grid_wait()
-__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Key tiles of sequence b (0 for an idle slot or an invalid length).
 __device__ __forceinline__ int flat_tiles(const FlatParams& p, int b) {
   const int len = __ldg(p.seqlens + b);
@@ -112,7 +108,6 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
   int* gave_up = misc + 8;  // [4] per compute warp, of the unit at hand
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_launch_next();
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&k_full[i], 1);

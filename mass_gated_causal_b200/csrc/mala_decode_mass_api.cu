@@ -45,6 +45,15 @@ int launch_flat(const CUtensorMap& mk, const CUtensorMap& mv, const mala::FlatPa
   return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
 }
 
+template <int D>
+int launch_mass(const mala::DecMassParams& m, unsigned grid, cudaStream_t st) {
+  if (m.G <= 1) mala::mala_decode_mass_kernel<D, 1><<<grid, mala::kDecMassThreads, 0, st>>>(m);
+  else if (m.G <= 2) mala::mala_decode_mass_kernel<D, 2><<<grid, mala::kDecMassThreads, 0, st>>>(m);
+  else if (m.G <= 4) mala::mala_decode_mass_kernel<D, 4><<<grid, mala::kDecMassThreads, 0, st>>>(m);
+  else mala::mala_decode_mass_kernel<D, 8><<<grid, mala::kDecMassThreads, 0, st>>>(m);
+  return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
+}
+
 template <int D, int BK, int GP>
 int launch(const CUtensorMap& mk, const CUtensorMap& mv, const mala::DecParams& p, cudaStream_t st) {
   using Lay = mala::DecLayout<D, BK, GP>;
@@ -188,9 +197,8 @@ int mala_decode_paged_mass(const void* q, const void* k_pages, const void* v_pag
   m.merge_blocks = merge_blocks;
   m.key_blocks = key_blocks;
   m.decay = decay;
-  // its launch overlaps the first kernel's end; it waits for that kernel itself
-  auto kern = d == 128 ? mala::mala_decode_mass_kernel<128> : mala::mala_decode_mass_kernel<64>;
-  return launch_dependent(kern, static_cast<unsigned>(blocks), mala::kDecMassThreads, st, m);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  return d == 128 ? launch_mass<128>(m, grid, st) : launch_mass<64>(m, grid, st);
 }
 
 }  // extern "C"

@@ -69,24 +69,6 @@ int set_smem(K kernel, int bytes) {
              : MALA_ERR_CUDA;
 }
 
-// Launch a kernel whose first act is griddepcontrol.wait, so that its launch may
-// overlap the end of the stream's previous kernel.
-template <typename P>
-int launch_dependent(void (*kernel)(P), unsigned grid, unsigned threads, cudaStream_t st, const P& params) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, params) == cudaSuccess) return MALA_OK;
-  cudaGetLastError();
-  return MALA_ERR_CUDA;
-}
-
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 inline int sm_count() {
