@@ -86,8 +86,8 @@ int launch_rope(mala::RopeParams p, int d, bool adjacent, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ evict
-template <int C>
-int launch_select(const mala::EvictParams& p, cudaStream_t st) {
+template <int C, int kKeep>
+int launch_select_keep(const mala::EvictParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * C);
   cfg.blockDim = dim3(mala::kEvictThreads);
@@ -98,11 +98,20 @@ int launch_select(const mala::EvictParams& p, cudaStream_t st) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, mala::mala_evict_select_kernel<C>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, mala::mala_evict_select_kernel<C, kKeep>, p) != cudaSuccess) {
     cudaGetLastError();
     return MALA_ERR_CUDA;
   }
   return MALA_OK;
+}
+
+template <int C>
+int launch_select(const mala::EvictParams& p, cudaStream_t st) {
+  // masses a thread meets in the longest row
+  const int each = (p.ld + C * mala::kEvictThreads - 1) / (C * mala::kEvictThreads);
+  if (each <= 4) return launch_select_keep<C, 4>(p, st);
+  if (each <= 16) return launch_select_keep<C, 16>(p, st);
+  return launch_select_keep<C, 0>(p, st);
 }
 
 }  // namespace
@@ -232,11 +241,11 @@ int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* inde
   p.status = status_ptr();
   if (!p.status) return MALA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // CTAs per row of masses: as many as keep all rows on the GPU at once (two
-  // CTAs to an SM), but no more than leave each 2K masses
+  // CTAs per row of masses: as many as keep all rows on the GPU at once (one
+  // CTA to an SM), but no more than leave each 2K masses
   const long long rows = static_cast<long long>(B) * Hkv;
   int cluster = 1;
-  while (cluster < 8 && rows * cluster <= sm_count() && ld_mass > 2048 * cluster) cluster *= 2;
+  while (cluster < 8 && rows * cluster * 2 <= sm_count() && ld_mass > 2048 * cluster) cluster *= 2;
   switch (cluster) {
     case 1: return launch_select<1>(p, st);
     case 2: return launch_select<2>(p, st);

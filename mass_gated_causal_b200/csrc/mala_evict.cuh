@@ -52,14 +52,14 @@ __device__ __forceinline__ uint32_t before_warp(const uint32_t* wsum, int warp, 
   return __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
 }
 
-template <int kCluster>
+template <int kCluster, int kKeep>
 __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const EvictParams p) {
   namespace cg = cooperative_groups;
   constexpr int NT = kEvictThreads, NW = NT / 32;
   static_assert(kEvictBins == 2 * NT, "two bins per thread");
   __shared__ __align__(16) uint32_t hist[3][kEvictBins];  // one per pass: no pass waits for the last one's readers
   __shared__ uint32_t wsum[NW], w_gt[NW], w_eq[NW];
-  __shared__ uint32_t s_digit, s_above;
+  __shared__ uint32_t s_digit, s_above, s_count;
   __shared__ uint32_t cta_cnt[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -105,10 +105,36 @@ __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const 
     if constexpr (kCluster == 1) __syncthreads();
     else cluster.sync();
   };
-  // this CTA's part of the rows between, in whole runs of 32 rows per warp
+  // this warp's part of the rows between: whole runs of 32 rows
   const int mid = hi - lo;
   const int per_warp = ((mid + kCluster * NW - 1) / (kCluster * NW) + 31) & ~31;
-  const int c0 = lo + min(rank * NW * per_warp, mid), c1 = lo + min((rank + 1) * NW * per_warp, mid);
+  const int w0 = lo + min((rank * NW + warp) * per_warp, mid);
+  const int w1 = min(w0 + per_warp, hi);
+  float kept[kKeep > 0 ? kKeep : 1];  // rows w0 + lane, w0 + lane + 32, ...
+  if constexpr (kKeep > 0) {
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int r = w0 + lane + 32 * i;
+      kept[i] = r < w1 ? mass[r] : 0.f;
+    }
+  }
+  // every row of the part, in order: f(row, mass, whether the row is there)
+  auto for_part = [&](auto&& f) {
+    if constexpr (kKeep > 0) {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        if (w0 + 32 * i >= w1) break;
+        const int r = w0 + lane + 32 * i;
+        f(r, kept[i], r < w1);
+      }
+    } else {
+#pragma unroll 8
+      for (int r0 = w0; r0 < w1; r0 += 32) {
+        const int r = r0 + lane;
+        f(r, r < w1 ? mass[r] : 0.f, r < w1);
+      }
+    }
+  };
 
 #pragma unroll
   for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(&hist[i][2 * tid]) = make_uint2(0u, 0u);
@@ -120,11 +146,10 @@ __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const 
     constexpr int kShift[3] = {21, 10, 0};
     const int shift = kShift[pass];
     const uint32_t bins = pass == 2 ? 1024u : 2048u;
-#pragma unroll 8
-    for (int r = c0 + tid; r < c1; r += NT) {
-      const uint32_t key = mass_key(mass[r]);
-      if ((key & mask) == prefix) atomicAdd(&hist[pass][(key >> shift) & (bins - 1)], 1u);
-    }
+    for_part([&](int, float x, bool there) {
+      const uint32_t key = mass_key(x);
+      if (there && (key & mask) == prefix) atomicAdd(&hist[pass][(key >> shift) & (bins - 1)], 1u);
+    });
     sync_all();
     // counts of this thread's two bins over the cluster; thread 0 takes the highest
     const int top = kEvictBins - 2 - 2 * tid;
@@ -150,22 +175,22 @@ __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const 
       const bool high = above + cnt.y >= remaining;
       s_digit = static_cast<uint32_t>(high ? top + 1 : top);
       s_above = high ? above : above + cnt.y;
+      s_count = high ? cnt.y : cnt.x;
     }
     __syncthreads();
     remaining -= s_above;
     prefix |= s_digit << shift;
     mask |= (bins - 1) << shift;
+    if (s_count == remaining) break;  // all of this digit's rows remain (the same for every CTA)
   }
 
-  // rows above the threshold, and the first `remaining` of those equal to it
-  const int w0 = min(c0 + warp * per_warp, c1), w1 = min(w0 + per_warp, c1);
+  // rows above the threshold, and the first `remaining` of those equal to it (by the digits read)
   uint32_t n_gt = 0, n_eq = 0;
-#pragma unroll 8
-  for (int r = w0 + lane; r < w1; r += 32) {
-    const uint32_t key = mass_key(mass[r]);
-    n_gt += key > prefix ? 1u : 0u;
-    n_eq += key == prefix ? 1u : 0u;
-  }
+  for_part([&](int, float x, bool there) {
+    const uint32_t key = mass_key(x) & mask;
+    n_gt += there && key > prefix ? 1u : 0u;
+    n_eq += there && key == prefix ? 1u : 0u;
+  });
   n_gt = __reduce_add_sync(0xffffffffu, n_gt);
   n_eq = __reduce_add_sync(0xffffffffu, n_eq);
   if (lane == 0) {
@@ -188,22 +213,19 @@ __global__ void __launch_bounds__(kEvictThreads) mala_evict_select_kernel(const 
     }
   }
   const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int r0 = w0; r0 < w1; r0 += 32) {
-    const int r = r0 + lane;
-    const float m = r < w1 ? mass[r] : 0.f;
-    const uint32_t key = mass_key(m);
-    const bool is_gt = r < w1 && key > prefix, is_eq = r < w1 && key == prefix;
+  for_part([&](int r, float x, bool there) {
+    const uint32_t key = mass_key(x) & mask;
+    const bool is_gt = there && key > prefix, is_eq = there && key == prefix;
     const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
     const uint32_t eq_rank = base_eq + __popc(be & below);
     if (is_gt || (is_eq && eq_rank < remaining)) {
       const int at = lo + static_cast<int>(base_gt + __popc(bg & below) + min(eq_rank, remaining));
       index[at] = r;
-      if (mass_out) mass_out[at] = m;
+      if (mass_out) mass_out[at] = x;
     }
     base_gt += __popc(bg);
     base_eq += __popc(be);
-  }
+  });
   if constexpr (kCluster > 1) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
