@@ -7,7 +7,7 @@
 // are recomputed tile by tile, as in the backward, and only their exponentials'
 // sums are kept.
 //
-// mala_key_mass_kernel: one CTA owns NT tiles of 128 keys of one (b, KV head) and
+// mala_key_mass_kernel: one CTA owns two tiles of 128 keys of one (b, KV head) and
 // walks the query tiles that see them, each for all heads of the GQA group. The
 // scores are computed transposed, S^T = K Q^T: the keys are the M rows, so a
 // thread owns one key (one TMEM lane) and its sum over the queries needs no
@@ -15,23 +15,22 @@
 // operand of every MMA; only Q passes through shared memory, which halves the
 // operand traffic of an MMA whose both operands lie there (at N = 128 that
 // traffic is as long as the MMA itself).
-//   warps 0 .. 8 NT - 1  compute: warps 8 x .. 8 x + 7 work on tile x, four on
-//              the first 64 queries of a query tile and four on the others; a
-//              thread reads its key's 64 scores out of TMEM, hands the columns
-//              back, and sums the exponentials
-//   warp  8 NT      producer: Q tiles by TMA and the rows' -LSE log2(e), a ring
-//   warp  8 NT + 1  MMA issuer (one thread), the tiles in turn
-// TMEM: S (NT x 128 columns) | K (NT x D / 2 columns).
+//   warps 0-15  compute: warps 8 x .. 8 x + 7 work on tile x, four on the first 64
+//               queries of a query tile and four on the others; a thread reads its
+//               key's 64 scores out of TMEM, hands the columns back, and sums the
+//               exponentials
+//   warp  16    producer: Q tiles by TMA and the rows' -LSE log2(e), a ring
+//   warp  17    MMA issuer (one thread), the tiles in turn
+// TMEM: S (2 x 128 columns) | K (2 x D / 2 columns).
 //
 // Bound: with d = 128 a 128 x 128 tile takes 512 cycles of MMA and 16,384
-// exponentials, 1,024 cycles at the special-function unit's 16 a cycle. So three
-// of every eight pairs are computed with packed FMAs instead (exp2_poly2): a
-// pair then costs 10 cycles of either unit, 640 a tile. Sixteen compute warps of
-// 64 scores (not eight of 128) leave registers to keep both units fed.
-//
-// NT = 2 reads each Q tile once for 256 keys; NT = 1 puts two CTAs on an SM, so
-// that one's start (tensor memory, K, the first Q tile) overlaps the other's
-// walk, which is what counts when a walk is short.
+// exponentials, 1,024 cycles at the special-function unit's 16 a cycle; one of
+// every eight pairs goes through packed FMAs instead (exp2_poly2). At 32K keys,
+// 32 heads over 8 KV heads, 4.5 ms (a tile every 1,240 cycles; the MMAs alone would
+// take 2.7 ms at the measured burst rate, the special-function unit 3.3 ms); the
+// GPU runs at its power limit by then (1,000 W at 1.8 GHz), so that more pairs on
+// the FMA pipes are slower although they relieve the unit (none 4.71 ms, one 4.51,
+// two 4.60, three 4.93).
 //
 // Splits: when the key tiles alone do not fill the GPU, each CTA takes
 // chunk_q query tiles and writes partial sums; mala_key_mass_join_kernel adds
@@ -50,7 +49,7 @@ struct KeyMassParams {
   int window;           // rows that count: the last `window` (0: all)
   int chunk_q;          // query tiles a CTA takes
   int n_chunks;         // grid: chunks per (b, KV head, key block)
-  int n_blocks;         // key blocks that the grid covers (NT x 128 keys each)
+  int n_blocks;         // key blocks that the grid covers (256 keys each)
   const uint16_t* k;    // [B, Lk, Hkv, d]
   const float* lse;     // [B, Hq, Lq]; packed batches: [Hq, total_q]
   const int* cu_q;      // packed batch (else null)
@@ -68,10 +67,14 @@ struct KeyMassParams {
   int stall_tile;  // test hook (-1: off): the MMA thread stalls before this item
 };
 
-template <int D, int NT>
+constexpr int kMassTiles = 2;                   // key tiles of a CTA
+constexpr int kMassKeys = kMassTiles * 128;     // its keys
+
+template <int D>
 struct KeyMassLayout {
-  static constexpr int NQ = NT == 2 ? 4 : 3;  // Q ring
-  static constexpr int CW = 8 * NT;           // compute warps
+  static constexpr int NT = kMassTiles;
+  static constexpr int NQ = 4;       // Q ring
+  static constexpr int CW = 8 * NT;  // compute warps
   static constexpr int THREADS = (CW + 2) * 32;
   static constexpr int Q_BYTES = 128 * D * 2;
   static constexpr int OFF_Q = 0;
@@ -82,11 +85,11 @@ struct KeyMassLayout {
   static constexpr int N_BARS = 2 * NQ + 2 * NT + 2;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
-  // so much that an SM holds no more CTAs than its tensor memory does (a further one would wait for it)
-  static constexpr int LEAST = NT == 2 ? 118 * 1024 : 78 * 1024;
+  // at least half of an SM's shared memory: a second CTA on the SM would wait for tensor memory
+  static constexpr int LEAST = 118 * 1024;
   static constexpr int ALLOC_BYTES = (BYTES > LEAST ? BYTES : LEAST) + 1024;
   static constexpr int COL_S = 0, COL_K = NT * 128;
-  static constexpr int TMEM_COLS = NT == 2 ? 512 : 256;
+  static constexpr int TMEM_COLS = 512;
   static_assert(ALLOC_BYTES <= 232448, "shared memory exceeds the per-CTA limit");
 };
 
@@ -152,13 +155,13 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
                  __uint_as_float(__float_as_uint(rhi) + (__float_as_uint(mhi) << 23)));
 }
 
-constexpr int kMassPoly = 1;  // of every eight packed pairs, how many go through exp2_poly2
+constexpr int kMassPoly = 1;  // of every eight packed pairs, how many go through exp2_poly2 (see above)
 
-template <int D, int NT>
-__global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
+template <int D>
+__global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
     mala_key_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const KeyMassParams p) {
-  using Lay = KeyMassLayout<D, NT>;
-  constexpr int NQ = Lay::NQ, CW = Lay::CW;
+  using Lay = KeyMassLayout<D>;
+  constexpr int NT = Lay::NT, NQ = Lay::NQ, CW = Lay::CW;
   constexpr uint32_t IDESC = idesc_bf16(128, 128, false, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
   const int bk = (static_cast<int>(blockIdx.x) / p.n_chunks) % (p.B * p.Hkv);
   const int blk = static_cast<int>(blockIdx.x) / (p.n_chunks * p.B * p.Hkv);
   const int b = bk / p.Hkv, hkv = bk % p.Hkv;
-  const int k0 = blk * (NT * 128);
+  const int k0 = blk * kMassKeys;
   const KeyMassSeq sq = key_mass_seq(p, b);
   if (!sq.ok) {  // nothing of this sequence is touched
     if (threadIdx.x == 0) atomicOr(p.status, kStatusSeqTable);
@@ -453,15 +456,16 @@ __global__ void __launch_bounds__(KeyMassLayout<D, NT>::THREADS, 3 - NT)
 }
 
 // Adds the chunks' partial sums of each key, in order, and the earlier mass.
-template <int NT>
-__global__ void __launch_bounds__(256) mala_key_mass_join_kernel(const KeyMassParams p) {
+// (A template so that more than one translation unit may include this file.)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) mala_key_mass_join_kernel(const KeyMassParams p) {
   const int bk = blockIdx.y, b = bk / p.Hkv;
-  const int key = blockIdx.x * 256 + threadIdx.x;
+  const int key = blockIdx.x * kThreads + threadIdx.x;
   const KeyMassSeq sq = key_mass_seq(p, b);
   if (!sq.ok || key >= p.ld) return;
   float sum = 0.f;
   if (key < sq.Lk) {
-    const int tiles = sq.n_qt - key_mass_qt0(sq, key & ~(NT * 128 - 1));
+    const int tiles = sq.n_qt - key_mass_qt0(sq, key & ~(kMassKeys - 1));
     const int n = tiles > 0 ? (tiles + p.chunk_q - 1) / p.chunk_q : 0;
     const float* src = p.part + static_cast<size_t>(bk) * p.n_chunks * p.part_ld + key;
 #pragma unroll 4

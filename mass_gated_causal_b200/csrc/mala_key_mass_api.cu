@@ -10,8 +10,6 @@ using namespace mala::host;
 
 namespace {
 
-constexpr int kLongWalk = 16;  // items (query tile, head) from which a CTA owns two key tiles
-
 // Columns of Q that mala_key_mass_window_kernel holds (rows of all heads, each
 // head's rounded up to 8), or 0 if it does not take the call.
 int window_cols(int G, int Lq, int window) {
@@ -21,7 +19,6 @@ int window_cols(int G, int Lq, int window) {
 }
 
 struct Plan {
-  int tiles;              // key tiles (of 128) a CTA owns
   int chunk_q, n_chunks;  // query tiles a CTA takes; chunks of the longest walk
   int blocks;             // key blocks of the longest sequence
   size_t part_bytes;
@@ -34,41 +31,40 @@ struct Plan {
 // 0.6 of an SM's share of all walks, the walks are whole: they start longest
 // first and the shorter ones even the SMs out. Above that, an SM that got the
 // longest walk would still run when the others are done, so the walks are cut
-// into chunks of half a share.
+// into chunks of half a share: 8K keys, 8 heads over 2 KV heads, 95 us against 289
+// with whole walks. Chunks of a quarter share cost more in starts than they even
+// out (108 us there, and 8K keys of 16 heads 175 us against 155 whole).
 Plan plan(double units, long long slots, int G, int Lq, int Lk, int window) {
   Plan w = {};
   if (window_cols(G, Lq, window) > 0) return w;  // Q fits in shared memory: the keys stream past it
   const int first = window > 0 && window < Lq ? Lq - window : 0;
   const long long n_qt = (Lq - first + 127) / 128;
-  // two key tiles to a CTA once its walk is long enough to hide its start
-  w.tiles = n_qt * G >= kLongWalk ? 2 : 1;
-  const int keys = w.tiles * 128, slots_per_sm = 3 - w.tiles;
-  w.blocks = (Lk + keys - 1) / keys;
+  w.blocks = (Lk + mala::kMassKeys - 1) / mala::kMassKeys;
   const long long seen = static_cast<long long>(Lk) - Lq + first;  // position of the first row that counts
-  const long long whole = std::min<long long>(w.blocks, seen / keys + 1), rest = w.blocks - whole;
-  const double walks = static_cast<double>(whole) * n_qt +
-                       std::max(0.0, static_cast<double>(rest) * (n_qt - 0.5 * w.tiles * (rest + 1)));
-  const double share = walks * units * G / (sm_count() * slots_per_sm);
+  const long long whole = std::min<long long>(w.blocks, seen / mala::kMassKeys + 1), rest = w.blocks - whole;
+  const double walks =
+      static_cast<double>(whole) * n_qt + std::max(0.0, static_cast<double>(rest) * (n_qt - (rest + 1)));
+  const double share = walks * units * G / sm_count();
   long long chunk = n_qt;
   if (static_cast<double>(n_qt) * G > 0.6 * share)
     chunk = std::max<long long>(1, std::min<long long>(n_qt, static_cast<long long>(std::ceil(0.5 * share / G))));
   w.chunk_q = static_cast<int>(chunk);
   w.n_chunks = static_cast<int>((n_qt + chunk - 1) / chunk);
   w.part_bytes =
-      w.n_chunks > 1 ? align256(static_cast<size_t>(slots) * w.n_chunks * w.blocks * keys * sizeof(float)) : 0;
+      w.n_chunks > 1 ? align256(static_cast<size_t>(slots) * w.n_chunks * w.blocks * mala::kMassKeys * sizeof(float)) : 0;
   return w;
 }
 
-template <int D, int NT>
+template <int D>
 int launch(const CUtensorMap& mq, const mala::KeyMassParams& p, unsigned grid, cudaStream_t st) {
-  using Lay = mala::KeyMassLayout<D, NT>;
-  auto kern = mala::mala_key_mass_kernel<D, NT>;
+  using Lay = mala::KeyMassLayout<D>;
+  auto kern = mala::mala_key_mass_kernel<D>;
   if (set_smem(kern, Lay::ALLOC_BYTES) != MALA_OK) return MALA_ERR_CUDA;
   kern<<<grid, Lay::THREADS, Lay::ALLOC_BYTES, st>>>(mq, p);
   if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
   if (p.n_chunks > 1) {
     const dim3 jg(static_cast<unsigned>((p.ld + 255) / 256), static_cast<unsigned>(p.B) * p.Hkv);
-    mala::mala_key_mass_join_kernel<NT><<<jg, 256, 0, st>>>(p);
+    mala::mala_key_mass_join_kernel<256><<<jg, 256, 0, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
   }
   return MALA_OK;
@@ -148,8 +144,8 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   p.chunk_q = w.chunk_q;
   p.n_chunks = w.n_chunks;
   // whole walks write the result, up to the end of its rows; chunks write partials
-  if (w.tiles > 0) p.n_blocks = w.n_chunks > 1 ? w.blocks : (ld + w.tiles * 128 - 1) / (w.tiles * 128);
-  p.part_ld = w.blocks * w.tiles * 128;
+  p.n_blocks = w.n_chunks > 1 ? w.blocks : (ld + mala::kMassKeys - 1) / mala::kMassKeys;
+  p.part_ld = w.blocks * mala::kMassKeys;
   p.k = static_cast<const uint16_t*>(k);
   p.lse = lse;
   p.cu_q = cu_q;
@@ -185,8 +181,7 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   if (!make_bshd_map(&mq, q, packed ? 1 : B, packed ? total_q : Lq, Hq, d, 128)) return MALA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned g = static_cast<unsigned>(grid);
-  if (d == 128) return w.tiles == 2 ? launch<128, 2>(mq, p, g, st) : launch<128, 1>(mq, p, g, st);
-  return w.tiles == 2 ? launch<64, 2>(mq, p, g, st) : launch<64, 1>(mq, p, g, st);
+  return d == 128 ? launch<128>(mq, p, g, st) : launch<64>(mq, p, g, st);
 }
 
 }  // namespace

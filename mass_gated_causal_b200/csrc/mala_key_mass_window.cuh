@@ -6,17 +6,20 @@
 // Q stays, K streams. One CTA takes one (b, KV head) and a run of its key tiles;
 // Q of all G heads is one operand of up to 512 columns, loaded once, so a key
 // tile costs its K and one MMA of N = kCols columns per half-row step, and no
-// start-up per key block (a walk per 128 keys, as in mala_key_mass_kernel, spent
-// 10 us on four query tiles).
+// start-up per key block (walks as in mala_key_mass_kernel took 174 us for the
+// case below, most of it the walks' starts).
 //   warps 0-15  compute: warp w owns the keys 32 (w % 4) .. + 31 of a tile and the
 //               columns (w / 4) kCols / 4 .. of a block; the four column groups'
 //               sums meet in shared memory, and group 0 writes the result
 //   warp  16    producer: Q once, K tiles through a ring
 //   warp  17    MMA issuer (one thread): S^T = K Q^T, two TMEM buffers in turn
 // Columns past a head's rows hold zeros in Q and -infinity in place of -LSE, so
-// they add nothing (at most 2^-126). Bound: G x W exponentials per key on the special-function
-// unit (at 256 columns 2,048 cycles a tile against 760 for reading K at the HBM
-// rate), which shares them with the FMA pipes (exp2_poly2).
+// they add nothing (at most 2^-126). Bound: G x W exponentials per key on the
+// special-function unit (at 256 columns 2,048 cycles a tile against 760 for reading
+// K at the HBM rate), a quarter of them moved to the FMA pipes (exp2_poly2). 64 rows
+// of 32 heads over 8 KV heads against 2 x 32,000 keys: 51 us (53 with an eighth, 56
+// with none, 51 with three eighths); one row, which only reads K, 33 us, of which
+// 21 are K's bytes.
 #pragma once
 
 #include "mala_key_mass.cuh"
