@@ -410,7 +410,9 @@ MALA_API int mala_decode_noalloc(const void* q, const void* kcache, const void* 
  *              outputs overlap neither inputs nor each other.
  *   strides    HOST int64 [12], in elements: (token, head) of q, k, v, q_out,
  *              k_out, v_out. Values of a head are adjacent. Multiples of 8, not
- *              negative; of the outputs at least d.
+ *              negative; an output's rows must not overlap: all heads of a
+ *              token before the next token, or all tokens of a head before the
+ *              next head (refused otherwise).
  *   positions  [n_axes, T] int32, in (any value, negative too)
  *   inv_freq   [rotary_dim / 2] fp32, in
  *   T >= 0 (0: nothing is done); d in {64, 128}; rotary_dim a multiple of 16,

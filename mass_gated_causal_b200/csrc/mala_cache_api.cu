@@ -48,11 +48,17 @@ int check_rope(int T, int Hq, int Hkv, int d, int rotary_dim, unsigned flags, un
 }
 
 // One strided tensor of rows: 16-byte chunks of every row aligned, and, for a
-// destination, rows that do not overlap.
+// destination, rows that do not overlap (all heads of a token before the next
+// token, or all tokens of a head before the next head).
 int check_rows(const void* x, long long tok, long long head, int T, int heads, int d, bool written) {
   if (!aligned16(x) || tok % 8 != 0 || head % 8 != 0) return MALA_ERR_UNSUPPORTED;
   if (tok < 0 || head < 0) return MALA_ERR_INVALID_ARG;
-  if (written && ((T > 1 && tok < d) || (heads > 1 && head < d))) return MALA_ERR_INVALID_ARG;
+  if (static_cast<double>(T - 1) * tok + static_cast<double>(heads - 1) * head >= static_cast<double>(1ll << 40))
+    return MALA_ERR_UNSUPPORTED;
+  if (written) {
+    if ((T > 1 && tok < d) || (heads > 1 && head < d)) return MALA_ERR_INVALID_ARG;
+    if (T > 1 && heads > 1 && tok < (heads - 1) * head + d && head < (T - 1) * tok + d) return MALA_ERR_INVALID_ARG;
+  }
   return MALA_OK;
 }
 
@@ -224,7 +230,9 @@ int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* inde
   if (new_seqlens == seqlens_k) return MALA_ERR_INVALID_ARG;  // other blocks still read the old lengths
   if (mass_out && (ld_mass_out < budget || mass_out == mass)) return MALA_ERR_INVALID_ARG;
   if (!aligned16(mass) || !aligned16(index) || (mass_out && !aligned16(mass_out))) return MALA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hkv >= (1ll << 24) || ld_mass > (1 << 30)) return MALA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv >= (1ll << 24) || ld_mass > (1 << 30) || budget > (1 << 30) ||
+      (mass_out && ld_mass_out > (1 << 30)))
+    return MALA_ERR_UNSUPPORTED;
   mala::EvictParams p = {};
   p.mass = mass;
   p.seqlens = seqlens_k;

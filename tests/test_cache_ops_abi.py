@@ -32,7 +32,8 @@ def strides(i, value):
     (dict(n_axes=0, sections=[]), 1), (dict(n_axes=5, sections=[16, 16, 16, 8, 8]), 1),
     (dict(sections=[32, 16, 15]), 1), (dict(sections=[80, -8, -8]), 1), (dict(sections=[32, 16, 24]), 1),
     (dict(sections=[16, 32, 16], flags=2), 1),  # more pairs than the turns of an axis
-    (dict(strides=strides(6, 120)), 1), (dict(strides=strides(7, 64)), 1), (dict(strides=strides(0, -1536)), 1),
+    (dict(strides=strides(6, 120)), 1), (dict(strides=strides(7, 64)), 1), (dict(strides=strides(6, 1016)), 1),
+    (dict(strides=strides(7, 1024)), 1), (dict(strides=strides(11, 1 << 62)), 2), (dict(strides=strides(6, 128)), 1), (dict(strides=strides(0, -1536)), 1),
     (dict(d=96), 2), (dict(d=256), 2), (dict(rotary_dim=120), 2), (dict(rotary_dim=0), 2), (dict(rotary_dim=144), 2),
     (dict(q=P + 8), 2), (dict(v_out=P + 2), 2), (dict(strides=strides(1, 132)), 2), (dict(strides=strides(8, 260)), 2),
 ])
@@ -163,6 +164,7 @@ def select(**kw):
     (dict(new_seqlens=2 * P), 1),  # the old lengths' array
     (dict(n_sink=(1 << 31) - 1, n_recent=(1 << 31) - 1), 1),
     (dict(mass=P + 8), 2), (dict(index=P + 4), 2), (dict(ld_mass=(1 << 30) + 1), 2),
+    (dict(budget=(1 << 30) + 1, mass_out=None), 2), (dict(ld_mass_out=(1 << 30) + 1), 2),
 ])
 def test_evict_select_rejects(kw, code):
     assert select(**kw) == code

@@ -136,6 +136,9 @@ def test_rope_layouts(cuda_lib):
     on_side = cuda_lib.rope(q, k, None, pos, f, sections=sec, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(on_side[0], want[0])
+    by_handle = cuda_lib.rope(q, k, None, pos, f, sections=sec, stream=0)  # the legacy default stream
+    torch.cuda.synchronize()
+    assert torch.equal(by_handle[0], want[0])
     empty = cuda_lib.rope(q[:0], k[:0], None, pos[:, :0].contiguous(), f, sections=sec)
     assert empty[0].shape == (0, 4, 128)
 
