@@ -594,10 +594,11 @@ def decode_paged_mass(q, k_pages, v_pages, block_table, seqlens_k, scale: float,
                                                          decay, out, n_splits, keep_map, workspace, stream)
 
 
-def evict_select(mass, seqlens_k, budget: int, n_sink: int = 0, n_recent: int = 0, stream=None):
+def evict_select(mass, seqlens_k, budget: int, n_sink: int = 0, n_recent: int = 0, mass_out=None, stream=None):
     """Rows that remain of each cache cut down to `budget` rows: mass [B,Hkv,ld] fp32, seqlens_k [B] int32 ->
-    (index [B,Hkv,budget] int32 ascending, -1 past the rows there are; new_seqlens [B]; mass [B,Hkv,budget])."""
-    return (_native or _load_native()).evict_select(mass, seqlens_k, budget, n_sink, n_recent, stream)
+    (index [B,Hkv,budget] int32 ascending, -1 past the rows there are; new_seqlens [B]; mass [B,Hkv,budget], or
+    mass_out [B,Hkv,ld'], ld' >= budget, filled with 0 past the rows: as long as the smaller cache's decode needs)."""
+    return (_native or _load_native()).evict_select(mass, seqlens_k, budget, n_sink, n_recent, mass_out, stream)
 
 
 def evict_gather(index, new_seqlens, k_pages, v_pages, block_table, out_table, k_out=None, v_out=None, stream=None):
@@ -608,9 +609,9 @@ def evict_gather(index, new_seqlens, k_pages, v_pages, block_table, out_table, k
 
 
 def evict(mass, seqlens_k, budget: int, k_pages, v_pages, block_table, out_table, n_sink: int = 0, n_recent: int = 0,
-          k_out=None, v_out=None, stream=None):
+          k_out=None, v_out=None, mass_out=None, stream=None):
     """Cut caches down to `budget` rows by collected weight (evict_select, then evict_gather) -> (index,
     new_seqlens, mass); the smaller caches are the pages of out_table."""
-    index, new, out = evict_select(mass, seqlens_k, budget, n_sink, n_recent, stream)
+    index, new, out = evict_select(mass, seqlens_k, budget, n_sink, n_recent, mass_out, stream)
     evict_gather(index, new, k_pages, v_pages, block_table, out_table, k_out, v_out, stream)
     return index, new, out

@@ -334,7 +334,8 @@ std::tuple<Tensor, Tensor, Tensor, OptTensor, int, Tensor> decode_paged_mass(
 }
 
 std::tuple<Tensor, Tensor, Tensor> evict_select(const Tensor& mass, const Tensor& seqlens_k, int64_t budget,
-                                                int64_t n_sink, int64_t n_recent, const py::object& stream) {
+                                                int64_t n_sink, int64_t n_recent, const OptTensor& mass_to,
+                                                const py::object& stream) {
   const char* where = "mala_evict_select";
   const Place place(where, mass, stream);
   place.need(mass, kF32);
@@ -343,11 +344,13 @@ std::tuple<Tensor, Tensor, Tensor> evict_select(const Tensor& mass, const Tensor
   const int64_t B = mass.size(0), Hkv = mass.size(1);
   place.shape(seqlens_k, "seqlens_k", {B});
   if (budget < 1) refuse(where, "budget must be at least 1, got ", budget);
-  const Tensor index = place.empty({B, Hkv, budget}, kI32), fresh = place.empty({B}, kI32),
-               out = place.empty({B, Hkv, budget}, kF32);
+  const Tensor index = place.empty({B, Hkv, budget}, kI32), fresh = place.empty({B}, kI32);
+  place.need(mass_to, kF32);
+  const Tensor out = mass_to ? *mass_to : place.empty({B, Hkv, budget}, kF32);
+  if (out.dim() != 3 || out.size(0) != B || out.size(1) != Hkv) refuse(where, "mass_out must be [", B, ", ", Hkv, ", ld]");
   check(mala_evict_select(fptr(mass), iptr(seqlens_k), iptr(index), iptr(fresh), fptr(out), c_int(where, B),
                           c_int(where, Hkv), c_int(where, mass.size(2)), c_int(where, budget), c_int(where, n_sink),
-                          c_int(where, n_recent), c_int(where, budget), place.handle()),
+                          c_int(where, n_recent), c_int(where, out.size(2)), place.handle()),
         where);
   return {index, fresh, out};
 }

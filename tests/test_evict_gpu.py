@@ -192,6 +192,10 @@ def test_binding_checks(cuda_lib):
             cuda_lib.evict_select(*args)
     with pytest.raises(cuda_lib.MalaError):
         cuda_lib.evict_select(m, sl, 5, n_sink=6)
+    with pytest.raises(cuda_lib.MalaError):
+        cuda_lib.evict_select(m, sl, 5, mass_out=torch.zeros(2, 4, 4, device="cuda"))
+    with pytest.raises(ValueError):
+        cuda_lib.evict_select(m, sl, 5, mass_out=torch.zeros(2, 3, 5, device="cuda"))
     index, new, _ = cuda_lib.evict_select(m, sl, 5)
     k, v = pools(4, 64, 4, 64, seed=1)
     t = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
