@@ -28,7 +28,8 @@
  *   - Device-side waits are bounded. If one expires the kernel records
  *     MALA_ERR_DEVICE_TIMEOUT in a device status word and returns;
  *     mala_check_status() reports it.
- *   - Calls are not reentrant with respect to the same output buffers.
+ *   - Calls are not reentrant with respect to the same output buffers or
+ *     workspaces.
  */
 #ifndef MALA_H_
 #define MALA_H_
@@ -340,7 +341,8 @@ MALA_API int mala_decode_exact(const void* q, const void* kcache, const void* vc
  * results equal mala_decode of the gathered cache with the same n_splits.
  *
  *   q          [B, Hq, d] bf16, in;  o [B, Hq, d] bf16, out;  lse [B, Hq] fp32, out
- *   k_pages, v_pages  [num_pages, page_size, Hkv, d] bf16, in
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, d] bf16, in (rows behind a
+ *              sequence's last key, too, hold finite values)
  *   block_table [B, max_pages_per_seq] int32, DEVICE memory (entries past a
  *              sequence's pages are not read)
  *   seqlens_k  [B] int32, DEVICE memory
@@ -527,7 +529,8 @@ MALA_API size_t mala_decode_mass_workspace_size(int B, int Hq, int Hkv, int d, i
  * to rounding: nothing is gated then, n_splits is not looked at, and the tiles of
  * all sequences are dealt evenly over the GPU). The newest key (j = seqlens_k[b]
  * - 1) is the query's own and starts from 0. A sequence of length 0 is an idle
- * slot: O = 0, LSE = -infinity, masses 0, no error.
+ * slot: O = 0, LSE = -infinity, masses 0, no error. Rows behind a sequence's last
+ * key may hold anything.
  *
  *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
  *   mass_out   [B, Hkv, ld_mass] fp32, out; entries past a sequence's keys

@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(320, 1)
   // kScores: this (b, KV head)'s scores, a row per head of the group
   const size_t score_ld = kScores ? static_cast<size_t>(p.max_pages) * BK : 0;
   float* score_row = kScores ? p.scores + static_cast<size_t>(b * p.Hkv + hkv) * G * score_ld : nullptr;
-  // paged: rows of the split's newest tile (always its first kept one) that hold keys. The rest
+  // kScores: rows of the split's newest tile (always its first kept one) that hold keys. The rest
   // of its page is whatever the pool held, perhaps not finite, and 0 times that is not 0.
-  const int live0 = kPaged ? Lk - (t1 - 1) * BK : BK;
+  const int live0 = kScores ? Lk - (t1 - 1) * BK : BK;
 
   float sc_cur[NR], sc_nxt[NR];  // scores (batched: my step's key, heads g0 ..; else head hh, every step)
   auto score = [&](int t, float (&sc)[NR]) {
@@ -488,7 +488,15 @@ __global__ void __launch_bounds__(320, 1)
     const int vs = n % NV, ps = n % NP;
     const bool okv = mbar_wait_warp(&v_full[vs], (n / NV) & 1, fs);
     if (!okv) { aborted = true; return; }
-    const int live_v = n == 0 ? live0 : BK;
+    if (kScores && n == 0 && live0 < BK) {  // once: the warp clears its own rows past the last key
+      for (int i = lane; i < KPWT * LPK; i += 32) {
+        const int j = warp * KPWT + i / LPK, ch = i % LPK;
+        if (j >= live0)
+          st_shared_v4(sVa + vs * TB + (ch >> 3) * (BK * 128) + sw128_offset(j, ch & 7), 0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();  // before the slot is loaded again
+      __syncwarp();
+    }
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
       const float al = sAlpha[ps * GP + g];
@@ -499,8 +507,8 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
     for (int s2 = 0; s2 < STEPS; ++s2) {
       const int j = warp * KPWT + s2 * KPW + kg;
-      uint32_t a[4] = {0u, 0u, 0u, 0u};
-      if (!kPaged || j < live_v) ld_shared_v4(row_addr(sVa + vs * TB, j), a[0], a[1], a[2], a[3]);
+      uint32_t a[4];
+      ld_shared_v4(row_addr(sVa + vs * TB, j), a[0], a[1], a[2], a[3]);
       uint64_t vf[4];
 #pragma unroll
       for (int e2 = 0; e2 < 4; ++e2) vf[e2] = bf16x2_to_f2(a[e2]);

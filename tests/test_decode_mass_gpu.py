@@ -106,8 +106,9 @@ def test_in_place_and_not_read(cuda_lib):
     assert torch.equal(none, cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.125, 0.0)[-1])
 
 
+@pytest.mark.parametrize("tau", [0.0, 1.0])
 @pytest.mark.parametrize("d,page,G", [(128, 128, 4), (64, 64, 1), (128, 64, 8), (64, 128, 3)])
-def test_what_lies_behind_the_keys_does_not_count(cuda_lib, d, page, G):
+def test_what_lies_behind_the_keys_does_not_count(cuda_lib, d, page, G, tau):
     """The last page's other rows and every other page hold NaN and infinities; idle slots have length 0."""
     lens = [page * 3 + 5, 0, 1, page]
     kp, vp, table = paged(4, max(lens), 2, d, page, seed=d)
@@ -117,22 +118,15 @@ def test_what_lies_behind_the_keys_does_not_count(cuda_lib, d, page, G):
     for b, n in enumerate(lens):
         for j in range(n):
             live[int(table[b, j // page]), j % page] = True
-    want = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.1, 0.0, n_splits=2)
+    want = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.1, tau, n_splits=2)
     kp[~live] = float("nan")
     vp[~live] = float("inf")
-    got = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.1, 0.0, n_splits=2)
+    got = cuda_lib.decode_paged_mass(q, kp, vp, table, sl, 0.1, tau, n_splits=2)
     assert cuda_lib.mala_check_status() == 0  # the idle slot is no error
     for x, y in ((want[0], got[0]), (want[1], got[1]), (want[2], got[2]), (want[5], got[5])):
         assert torch.equal(x, y)
     assert bool((got[0][1] == 0).all()) and bool((got[1][1] == float("-inf")).all()) and bool((got[5][1] == 0).all())
     assert bool(torch.isfinite(got[0].float()).all())
-    # the same tails under the plain paged decode (which has no idle slots)
-    o = cuda_lib.decode_paged(q[[0, 2, 3]].contiguous(), kp, vp, table[[0, 2, 3]].contiguous(),
-                              sl[[0, 2, 3]].contiguous(), 0.1, 0.0, n_splits=2)[0]
-    assert bool(torch.isfinite(o.float()).all())
-    # two kernels: each within half a bf16 step and the sums' rounding of the same value
-    same = got[0][[0, 2, 3]].float()
-    assert bool(((o.float() - same).abs() <= 2.0 ** -7 * same.abs() + 1e-4 * float(same.abs().max())).all())
 
 
 def test_bad_tables_are_reported(cuda_lib):
