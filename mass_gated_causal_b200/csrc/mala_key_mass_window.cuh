@@ -243,6 +243,58 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
     };
     for (int t = 0; t < AHEAD; ++t) fetch_old(t, t);
     int slot = 0;
+    // this key's weights summed over the warp's columns of block y, whose scores are in buffer buf;
+    // kPlain: every row sees every key of the tile
+    auto strip = [&](auto plain_c, int buf, int y, int key) -> float {
+      constexpr bool kPlain = decltype(plain_c)::value;
+      const uint32_t tS = tmem + buf * 256 + cg * CG + lane_base;
+      const uint32_t la = lse_a + y * kCols * 4;
+      uint64_t acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
+#pragma unroll
+      for (int c0 = 0; c0 < CG; c0 += 32) {
+        constexpr int kLast = (CG - 1) / 32 * 32;
+        uint32_t sv[32];
+        if (CG - c0 >= 32) tmem_ld32(tS + c0, sv);
+        else tmem_ld16(tS + c0, *reinterpret_cast<uint32_t(*)[16]>(sv));
+        tmem_ld_wait();
+        if (c0 == kLast) {  // the block is out of TMEM: its columns go back to the MMA issuer
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[buf]);
+        }
+#pragma unroll
+        for (int j = 0; j < 32 && c0 + j < CG; j += 16) {
+          uint64_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (c0 + j + 2 * e) * 4, v[e], v[e + 1]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
+          const int* pos = sPos + y * kCols + cg * CG + c0 + j;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (kPlain && e % 2 == 1 && e < 2 * kWinPoly) {
+              v[e] = exp2_poly2(v[e]);
+            } else {
+              float lo, hi;
+              f2_unpack(v[e], lo, hi);
+              if (!kPlain) {
+                lo = key <= pos[2 * e] ? lo : -INFINITY;
+                hi = key <= pos[2 * e + 1] ? hi : -INFINITY;
+              }
+              v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e & 3] = f2_add(acc[e & 3], v[e]);
+        }
+      }
+      float lo, hi;
+      f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
+      return lo + hi;
+    };
     int n = 0;
     for (int t = 0; t < T; ++t) {
       const int k0 = (t0 + t) * 128, key = k0 + tid;
@@ -254,60 +306,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
         if (!aborted) aborted = !mbar_wait_warp(&s_full[n & 1], (n >> 1) & 1, fs);
         if (aborted) continue;  // the barriers below are still met
         tc_fence_after();
-        const uint32_t tS = tmem + (n & 1) * 256 + cg * CG + lane_base;
-        const uint32_t la = lse_a + y * kCols * 4;
-        uint64_t acc[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
-#pragma unroll
-        for (int c0 = 0; c0 < CG; c0 += 32) {
-          constexpr int kLast = (CG - 1) / 32 * 32;
-          uint32_t sv[32];
-          if (CG - c0 >= 32) tmem_ld32(tS + c0, sv);
-          else tmem_ld16(tS + c0, *reinterpret_cast<uint32_t(*)[16]>(sv));
-          tmem_ld_wait();
-          if (c0 == kLast) {  // the block is out of TMEM: its columns go back to the MMA issuer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[n & 1]);
-          }
-#pragma unroll
-          for (int j = 0; j < 32 && c0 + j < CG; j += 16) {
-            uint64_t v[8];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (c0 + j + 2 * e) * 4, v[e], v[e + 1]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
-            if (plain) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if (e % 2 == 1 && e < 2 * kWinPoly) {
-                  v[e] = exp2_poly2(v[e]);
-                } else {
-                  float lo, hi;
-                  f2_unpack(v[e], lo, hi);
-                  v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
-                }
-              }
-            } else {
-              const int* pos = sPos + y * kCols + cg * CG + c0 + j;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float lo, hi;
-                f2_unpack(v[e], lo, hi);
-                lo = key <= pos[2 * e] ? lo : -INFINITY;
-                hi = key <= pos[2 * e + 1] ? hi : -INFINITY;
-                v[e] = f2_pack(ex2_approx(lo), ex2_approx(hi));
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e & 3] = f2_add(acc[e & 3], v[e]);
-          }
-        }
-        float lo, hi;
-        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
-        sum += lo + hi;
+        sum += plain ? strip(std::true_type(), n & 1, y, key) : strip(std::false_type(), n & 1, y, key);
       }
       float* red = sRed + (t & 1) * 512;
       red[cg * 128 + tid] = sum;
