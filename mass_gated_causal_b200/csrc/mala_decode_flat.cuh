@@ -21,6 +21,13 @@
 // as rows 0-7 and 8-15 of one operand, so that P loses nothing at bf16 size (hi and
 // lo hold 16 bits) and the second half of the rows is not wasted. On the FMA pipes
 // the same products took 3,500 cycles a tile pair, more than HBM needs.
+//
+// Short caches (kShort): a cluster of CTAs takes one (sequence, KV head), its
+// tiles dealt in turn, and everything ends there: the scores stay in shared
+// memory, the CTAs read each other's maxima, sums and O through distributed shared
+// memory, and each writes a slice of O and the masses of its own keys. One launch,
+// no workspace: 2 sequences of up to 2K keys, 2 KV heads, 7.5 us in a graph against
+// 12.5 for the two kernels.
 #pragma once
 
 #include "mala_ptx.cuh"
@@ -42,11 +49,24 @@ struct FlatParams {
   unsigned* status;
   uint64_t wait_ns;
   int stall_tile;
+  // kShort only (the others' are written by the second kernel)
+  uint16_t* o;           // [B, Hq, d]
+  float* lse;            // [B, Hq]
+  const float* mass_in;  // [B, Hkv, ld], nullable
+  float* mass_out;
+  int32_t* kept_tiles;
+  uint8_t* keep_map;
+  float decay;
+  int ld;
+  int cluster;  // CTAs per (sequence, KV head)
+  int pitch;    // floats between the heads' scores in shared memory
 };
 
 constexpr int kFlatTile = 64;      // keys per tile
 constexpr int kFlatLeastRun = 2;   // tiles: a run is not cut shorter
 constexpr int kFlatThreads = 160;
+constexpr int kShortTiles = 8;     // kShort: tiles a CTA takes at most
+constexpr int kShortCluster = 16;  // and CTAs of a cluster
 
 template <int D>
 struct FlatLayout {
@@ -58,7 +78,20 @@ struct FlatLayout {
   static constexpr int OFF_MISC = OFF_BAR + 3 * NS * 8;  // k_full, v_full, empty
   static constexpr int BYTES = OFF_MISC + 48;
   static constexpr int ALLOC_BYTES = BYTES + 1024;
-  static_assert(ALLOC_BYTES <= 113 * 1024, "two CTAs to an SM");
+  static constexpr int PAIR_BYTES = 113 * 1024;  // two CTAs to an SM
+  static_assert(ALLOC_BYTES <= PAIR_BYTES);
+
+  // kShort: the warps' partials take the first stage once its tiles are read, and
+  // the scores, [G][pitch] fp32, lie behind the rest. Eight floats more than the
+  // tiles fill put the heads of a warp's stores into different banks.
+  static constexpr int SHORT_NS = D == 128 ? 3 : 4;
+  static constexpr int SHORT_ML = 2 * SHORT_NS * T_BYTES;
+  static constexpr int SHORT_BAR = SHORT_ML + 2 * 4 * 8 * 4;
+  static constexpr int SHORT_MISC = SHORT_BAR + 3 * SHORT_NS * 8;
+  static constexpr int SHORT_SCORES = SHORT_MISC + 48;
+  static constexpr int short_pitch(int tiles) { return tiles * kFlatTile + 8; }
+  static constexpr int short_bytes(int G, int tiles) { return SHORT_SCORES + G * short_pitch(tiles) * 4 + 1024; }
+  static_assert(2 * 8 * D * 4 <= 2 * T_BYTES && SHORT_SCORES % 8 == 0);
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -88,22 +121,22 @@ __device__ __forceinline__ int flat_tiles(const FlatParams& p, int b) {
   return len < 0 || len > p.max_len ? 0 : (len + kFlatTile - 1) / kFlatTile;
 }
 
-template <int D>
+template <int D, bool kShort>
 __global__ void __launch_bounds__(kFlatThreads, 2)
     mala_decode_flat_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const FlatParams p) {
   using Lay = FlatLayout<D>;
-  constexpr int NS = Lay::NS, TB = Lay::T_BYTES;
+  constexpr int NS = kShort ? Lay::SHORT_NS : Lay::NS, TB = Lay::T_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;  // stage s: K at 2 s TB, V at (2 s + 1) TB
-  float* sRed = reinterpret_cast<float*>(smem + Lay::OFF_RED);
-  float* sM = reinterpret_cast<float*>(smem + Lay::OFF_ML);
+  float* sRed = reinterpret_cast<float*>(smem + (kShort ? 0 : Lay::OFF_RED));
+  float* sM = reinterpret_cast<float*>(smem + (kShort ? Lay::SHORT_ML : Lay::OFF_ML));
   float* sL = sM + 32;
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + (kShort ? Lay::SHORT_BAR : Lay::OFF_BAR));
   uint64_t* v_full = k_full + NS;
   uint64_t* empty = v_full + NS;
-  int* misc = reinterpret_cast<int*>(smem + Lay::OFF_MISC);
+  int* misc = reinterpret_cast<int*>(smem + (kShort ? Lay::SHORT_MISC : Lay::OFF_MISC));
   int* abort_flag = misc;  // then: first sequence, its first tile, the run's length, tiles in all
   int* gave_up = misc + 8;  // [4] per compute warp, of the unit at hand
 
@@ -117,7 +150,7 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) {
+  if (!kShort && warp == 0) {
     // tiles in all, the run length, and the sequence in which this CTA's run begins
     long long all = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -160,11 +193,13 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
     }
   }
   __syncthreads();
-  const int run = misc[3], all = misc[4];
-  const long long begin = static_cast<long long>(blockIdx.x) * run;
-  if (begin >= all) return;
+  const int run = kShort ? 1 : misc[3], all = kShort ? 0 : misc[4];
+  const long long begin = kShort ? 0 : static_cast<long long>(blockIdx.x) * run;
+  if (!kShort && begin >= all) return;
   const int pos0 = static_cast<int>(begin), pos1 = min(all, pos0 + run);
   const FailState fs{abort_flag, p.status, p.wait_ns};
+  const int rank = kShort ? static_cast<int>(blockIdx.x) % p.cluster : 0;
+  const int step = kShort ? p.cluster : 1;  // between the tiles of a walk
 
   // A walk over the run: unit (b, hkv) and its tiles [t, t1) in the run.
   struct Walk {
@@ -172,6 +207,15 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
   };
   auto start = [&]() {
     Walk w;
+    if constexpr (kShort) {
+      const int unit = static_cast<int>(blockIdx.x) / p.cluster;
+      w.b = unit / p.Hkv;
+      w.hkv = unit % p.Hkv;
+      w.nt = w.t1 = flat_tiles(p, w.b);
+      w.t = rank;
+      w.at = 0;
+      return w;
+    }
     w.b = misc[1];
     w.nt = flat_tiles(p, w.b);
     w.hkv = (pos0 - misc[2]) / w.nt;
@@ -181,6 +225,7 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
     return w;
   };
   auto next = [&](Walk& w) {  // false: the run ends with this unit
+    if constexpr (kShort) return false;
     w.at += w.nt;
     if (w.at >= pos1) return false;
     if (++w.hkv == p.Hkv) {
@@ -196,23 +241,26 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const int shift = p.page_shift - 6, sub = (1 << shift) - 1;  // tiles of a page
-      // the page of a tile, checked: an id outside the pool is reported and read as
-      // zeros (a TMA load outside the tensor fills)
-      auto page_of = [&](const Walk& w, int t) {
-        const int pg = __ldg(p.block_table + static_cast<size_t>(w.b) * p.max_pages + (t >> shift));
+      auto page_at = [&](int b, int t) { return __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + (t >> shift)); };
+      // an id outside the pool is reported and read as zeros (a TMA load outside the tensor fills)
+      auto checked = [&](int pg) {
         if (pg >= 0 && pg < p.num_pages) return pg;
         atomicOr(p.status, kStatusSeqTable);
         return p.num_pages;
       };
+      // kShort: the first page id is on its way while the length is (perhaps one past the last page: not used then)
+      const int pg_first = kShort ? page_at(static_cast<int>(blockIdx.x) / p.cluster / p.Hkv,
+                                            min(rank, ((p.max_pages - 1) << shift)))
+                                  : 0;
       Walk w = start();
       int n = 0, st = 0;
       uint32_t par = 1;
       bool ok = true;
       do {
-        int pg_next = page_of(w, w.t);  // page ids are read a tile ahead
-        for (int t = w.t; ok && t < w.t1; ++t, ++n) {
-          const int pg = pg_next;
-          if (t + 1 < w.t1) pg_next = page_of(w, t + 1);
+        int pg_next = kShort ? pg_first : page_at(w.b, w.t);  // page ids are read a tile ahead
+        for (int t = w.t; ok && t < w.t1; t += step, ++n) {
+          const int pg = checked(pg_next);
+          if (t + step < w.t1) pg_next = page_at(w.b, t + step);
           if (n >= NS && !mbar_wait(&empty[st], par, fs)) {
             ok = false;
             break;
@@ -241,6 +289,13 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
         mbar_wait_drain(&v_full[i % NS], (i / NS) & 1);
       }
     }
+    if constexpr (kShort) {  // the cluster's two barriers count every thread
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
+    }
     return;  // the other warps synchronise with named barrier 1
   }
 
@@ -257,7 +312,7 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
   bool aborted = false;
   Walk w = start();
   do {
-    const int len = __ldg(p.seqlens + w.b);
+    const int len = kShort && w.nt == 0 ? 0 : __ldg(p.seqlens + w.b);
     const int unit = w.b * p.Hkv + w.hkv;
     uint32_t qa[D / 16][2];  // rows 0-7 of Q; rows 8-15 are zero
 #pragma unroll
@@ -276,9 +331,27 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     float m = -INFINITY, l = 0.f;
-    float* score = p.scores + (static_cast<size_t>(unit) * p.G + g) * p.max_len + warp * 16 + 2 * c;
+    float* score;  // of head g and this lane's keys in a tile
+    if constexpr (kShort) {
+      score = reinterpret_cast<float*>(smem + Lay::SHORT_SCORES) + g * p.pitch + warp * 16 + 2 * c;
+      const size_t row = static_cast<size_t>(unit) * p.ld;
+      for (int j = w.nt * kFlatTile + rank * 128 + static_cast<int>(threadIdx.x); j < p.ld; j += step * 128)
+        p.mass_out[row + j] = 0.f;
+      if (rank == 0) {
+        const int pages = (len + (1 << p.page_shift) - 1) >> p.page_shift;
+        const size_t first = static_cast<size_t>(w.b) * p.Hq + w.hkv * p.G;
+        if (static_cast<int>(threadIdx.x) < p.G) p.kept_tiles[first + threadIdx.x] = pages;
+        if (p.keep_map != nullptr)
+          for (int h = 0; h < p.G; ++h)
+            for (int i = threadIdx.x; i < pages; i += 128) p.keep_map[(first + h) * p.max_pages + i] = 1;
+        const int given = __ldg(p.seqlens + w.b);
+        if (w.hkv == 0 && threadIdx.x == 0 && (given < 0 || given > p.max_len)) atomicOr(p.status, kStatusSeqTable);
+      }
+    } else {
+      score = p.scores + (static_cast<size_t>(unit) * p.G + g) * p.max_len + warp * 16 + 2 * c;
+    }
 
-    for (int t = w.t; t < w.t1; ++t) {
+    for (int t = w.t; t < w.t1; t += step) {
       const uint32_t kt = kv + 2 * st * TB, vt = kt + TB;
       if (!aborted) aborted = !mbar_wait_warp(&k_full[st], par, fs);
       if (aborted) break;
@@ -297,8 +370,10 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
       float x[4] = {s[0][0] * p.scale_log2, s[0][1] * p.scale_log2, s[1][0] * p.scale_log2, s[1][1] * p.scale_log2};
       const int key0 = t * kFlatTile + warp * 16;
       if (g < p.G) {
-        *reinterpret_cast<float2*>(score + t * kFlatTile) = make_float2(x[0], x[1]);
-        *reinterpret_cast<float2*>(score + t * kFlatTile + 8) = make_float2(x[2], x[3]);
+        float* to = kShort ? score : score + t * kFlatTile;
+        *reinterpret_cast<float2*>(to) = make_float2(x[0], x[1]);
+        *reinterpret_cast<float2*>(to + 8) = make_float2(x[2], x[3]);
+        if constexpr (kShort) score += kFlatTile;
       }
       const bool tail = key0 + 16 > len;  // uniform over the warp: some of its keys are past the last
       if (tail) {
@@ -357,6 +432,18 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
       }
     }
 
+    float before[kShortTiles / 2];  // kShort: earlier masses of this thread's keys, on their way while the cluster meets
+    if constexpr (kShort) {
+#pragma unroll
+      for (int u = 0; u < kShortTiles / 2; ++u) {
+        const int i = static_cast<int>(threadIdx.x) + 128 * u;
+        const int j = (rank + (i >> 6) * step) * kFlatTile + (i & 63);
+        before[u] = p.mass_in != nullptr && p.decay != 0.f && j < len - 1
+                        ? p.mass_in[static_cast<size_t>(unit) * p.ld + j]
+                        : 0.f;
+      }
+    }
+
     // the unit's part of this run: the warps' results into one
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -391,6 +478,74 @@ __global__ void __launch_bounds__(kFlatThreads, 2)
       }
     }
     named_bar_sync(1, 128);
+    if constexpr (kShort) {
+      const int tid = threadIdx.x, n_cta = p.cluster;
+      // this CTA's O (relative to its maxima), maxima and sums, for the cluster to read
+      if (warp == 0) {
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          const float2 v = *reinterpret_cast<const float2*>(sRed + 8 * D + g * D + j * 8 + 2 * c);
+          *reinterpret_cast<float2*>(sRed + g * D + j * 8 + 2 * c) = make_float2(o[j][0] + v.x, o[j][1] + v.y);
+        }
+        if (c == 0) {
+          sM[g] = top;
+          sL[g] = z;
+        }
+      }
+      cluster_arrive();
+      cluster_wait();
+      // weight of CTA r in head h, and the heads' LSEs (log2 units): 16 threads a head
+      float* weight = sRed + 8 * D;  // [8][kShortCluster]
+      float* lse2 = weight + 8 * kShortCluster;
+      {
+        const int h = tid / kShortCluster, r = tid % kShortCluster;
+        float mt = -INFINITY, zt = 0.f;
+        if (r < n_cta) {
+          mt = ld_cluster_f32(sM + h, r);
+          zt = ld_cluster_f32(sL + h, r);
+        }
+        float mx = mt;
+#pragma unroll
+        for (int i = kShortCluster / 2; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+        const float e = mt == -INFINITY ? 0.f : ex2_approx(mt - mx);
+        float sum = zt * e;
+#pragma unroll
+        for (int i = kShortCluster / 2; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+        weight[tid] = sum > 0.f ? e / sum : 0.f;
+        const float l2 = sum > 0.f ? mx + lg2_approx(sum) : -INFINITY;
+        if (r == 0) lse2[h] = l2;
+        if (r == 0 && rank == 0 && h < p.G)
+          p.lse[static_cast<size_t>(w.b) * p.Hq + w.hkv * p.G + h] = l2 * 0.69314718055994531f;
+      }
+      named_bar_sync(1, 128);
+      // a slice of O: pairs of values rank, rank + cluster, ..
+      for (int i = rank + n_cta * tid; i < p.G * (D / 2); i += n_cta * 128) {
+        const int h = i / (D / 2), e = i % (D / 2) * 2;
+        float x = 0.f, y = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < n_cta; ++r) {
+          const float2 v = ld_cluster_2f32(sRed + h * D + e, r);
+          const float f = weight[h * kShortCluster + r];
+          x = fmaf(f, v.x, x);
+          y = fmaf(f, v.y, y);
+        }
+        *reinterpret_cast<uint32_t*>(p.o + (static_cast<size_t>(w.b) * p.Hq + w.hkv * p.G + h) * D + e) =
+            pack_bf16x2(x, y);
+      }
+      cluster_arrive();  // the others' shared memory is read
+      const float* sc = reinterpret_cast<const float*>(smem + Lay::SHORT_SCORES);
+#pragma unroll
+      for (int u = 0; u < kShortTiles / 2; ++u) {
+        const int i = tid + 128 * u, t = rank + (i >> 6) * step;
+        if (t >= w.nt) break;
+        const int j = t * kFlatTile + (i & 63);
+        float mass = 0.f;
+        for (int h = 0; h < p.G; ++h) mass += ex2_approx(sc[h * p.pitch + i] - lse2[h]);
+        p.mass_out[static_cast<size_t>(unit) * p.ld + j] = j < len ? fmaf(p.decay, before[u], mass) : 0.f;
+      }
+      cluster_wait();  // no CTA leaves while another may read its shared memory
+      return;
+    }
     if (warp == 0 && g < p.G && !aborted) {
       const int slot = static_cast<int>(blockIdx.x) - w.at / run;
       const size_t at = (static_cast<size_t>(w.b) * p.Hq + w.hkv * p.G + g) * p.slots + slot;
