@@ -488,7 +488,7 @@ MALA_API size_t mala_key_mass_varlen_workspace_size(int num_seqs, int Hq, int Hk
  *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
  *   mass_out   [B, Hkv, ld_mass] fp32, out; entries j >= Lk become 0. May be
  *              mass_in.
- *   ld_mass >= Lk, decay >= 0, window >= 0; workspace 256-byte aligned, >=
+ *   Lk <= ld_mass <= 2^30, decay >= 0, window >= 0; workspace 256-byte aligned, >=
  *   mala_key_mass_workspace_size(...) bytes (NULL if that is 0)
  */
 MALA_API int mala_key_mass(const void* q, const void* k, const float* lse, const float* mass_in, float* mass_out,
@@ -535,7 +535,7 @@ MALA_API size_t mala_decode_mass_workspace_size(int B, int Hq, int Hkv, int d, i
  *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
  *   mass_out   [B, Hkv, ld_mass] fp32, out; entries past a sequence's keys
  *              become 0. May be mass_in.
- *   ld_mass >= max_pages_per_seq * page_size; decay >= 0
+ *   max_pages_per_seq * page_size <= ld_mass <= 2^30; decay >= 0
  *   workspace  >= mala_decode_mass_workspace_size(...) bytes, 256-byte aligned
  */
 MALA_API int mala_decode_paged_mass(const void* q, const void* k_pages, const void* v_pages,

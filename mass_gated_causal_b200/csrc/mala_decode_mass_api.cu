@@ -146,6 +146,7 @@ int mala_decode_paged_mass(const void* q, const void* k_pages, const void* v_pag
   if (rc != MALA_OK) return rc;
   if (!(decay >= 0.f) || !std::isfinite(decay) || ld_mass < Lk) return MALA_ERR_INVALID_ARG;
   if (!aligned16(mass_out) || (mass_in && !aligned16(mass_in))) return MALA_ERR_UNSUPPORTED;
+  if (ld_mass > (1 << 30)) return MALA_ERR_UNSUPPORTED;  // keys are counted in 32 bits, in blocks past the end too
   if (static_cast<long long>(num_pages) * page_size * Hkv * d >= (1ll << 40)) return MALA_ERR_UNSUPPORTED;
   // without a gate the tiles are dealt evenly over the GPU, whatever n_splits says
   const bool gate = tau > 0.f;

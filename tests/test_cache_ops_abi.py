@@ -132,6 +132,7 @@ def decode(**kw):
     (dict(tau=-1.0), 1), (dict(decay=-1.0), 1), (dict(decay=float("inf")), 1), (dict(ld_mass=40 * 128 - 1), 1),
     (dict(page_size=256), 2), (dict(d=96), 2), (dict(Hq=64, Hkv=2), 2), (dict(max_pages_per_seq=1 << 24), 2),
     (dict(k_pages=P + 8), 2), (dict(mass_out=P + 4), 2), (dict(n_splits=70000, ld_mass=1 << 20), 2),
+    (dict(ld_mass=(1 << 30) + 1), 2), (dict(ld_mass=(1 << 31) - 1), 2),
     (dict(workspace=None), 3), (dict(workspace_bytes=1000), 3), (dict(workspace=P + 64), 3),
 ])
 def test_decode_paged_mass_rejects(kw, code):
