@@ -612,6 +612,5 @@ def evict(mass, seqlens_k, budget: int, k_pages, v_pages, block_table, out_table
           k_out=None, v_out=None, mass_out=None, stream=None):
     """Cut caches down to `budget` rows by collected weight (evict_select, then evict_gather) -> (index,
     new_seqlens, mass); the smaller caches are the pages of out_table."""
-    index, new, out = evict_select(mass, seqlens_k, budget, n_sink, n_recent, mass_out, stream)
-    evict_gather(index, new, k_pages, v_pages, block_table, out_table, k_out, v_out, stream)
-    return index, new, out
+    return (_native or _load_native()).evict(mass, seqlens_k, budget, k_pages, v_pages, block_table, out_table, n_sink,
+                                             n_recent, k_out, v_out, mass_out, stream)

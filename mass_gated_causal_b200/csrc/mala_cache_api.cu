@@ -96,6 +96,10 @@ int launch_rope(mala::RopeParams p, int d, bool adjacent, cudaStream_t st) {
 // ------------------------------------------------------------------ evict
 template <int C, int kKeep>
 int launch_select_keep(const mala::EvictParams& p, cudaStream_t st) {
+  if constexpr (C == 1) {
+    mala::mala_evict_select_kernel<C, kKeep><<<static_cast<unsigned>(p.B) * p.Hkv, mala::kEvictThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * C);
   cfg.blockDim = dim3(mala::kEvictThreads);

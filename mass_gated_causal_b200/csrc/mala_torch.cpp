@@ -42,8 +42,10 @@ struct Place {
   const char* where;
   c10::DeviceIndex dev;
   c10::cuda::CUDAStream stream;
+  bool current;  // torch's current stream
 
-  Place(const char* where_, const Tensor& x, const py::object& s) : where(where_), dev(device(where_, x)), stream(pick(dev, s)) {}
+  Place(const char* where_, const Tensor& x, const py::object& s)
+      : where(where_), dev(device(where_, x)), stream(pick(dev, s)), current(stream == c10::cuda::getCurrentCUDAStream(dev)) {}
 
   static c10::DeviceIndex device(const char* where, const Tensor& x) {
     if (!x.is_cuda() || x.get_device() != c10::cuda::current_device())
@@ -69,7 +71,8 @@ struct Place {
     if (x.sizes() != want) refuse(where, name, " must have shape ", want, ", got ", x.sizes());
   }
   Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
-    c10::cuda::CUDAStreamGuard guard(stream);
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    if (!current) guard.reset_stream(stream);
     return at::empty(size, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, dev)));
   }
   // (pointer, bytes) of the workspace: the caller's, or a new one, kept in `hold`
@@ -382,6 +385,17 @@ std::tuple<Tensor, Tensor> evict_gather(const Tensor& index, const Tensor& new_s
   return {ko, vo};
 }
 
+std::tuple<Tensor, Tensor, Tensor> evict(const Tensor& mass, const Tensor& seqlens_k, int64_t budget,
+                                         const Tensor& k_pages, const Tensor& v_pages, const Tensor& block_table,
+                                         const Tensor& out_table, int64_t n_sink, int64_t n_recent,
+                                         const OptTensor& k_out, const OptTensor& v_out, const OptTensor& mass_to,
+                                         const py::object& stream) {
+  auto rows_left = evict_select(mass, seqlens_k, budget, n_sink, n_recent, mass_to, stream);
+  evict_gather(std::get<0>(rows_left), std::get<1>(rows_left), k_pages, v_pages, block_table, out_table, k_out, v_out,
+               stream);
+  return rows_left;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(mala_torch, m) {
@@ -396,4 +410,5 @@ PYBIND11_MODULE(mala_torch, m) {
   m.def("decode_paged_mass", &decode_paged_mass);
   m.def("evict_select", &evict_select);
   m.def("evict_gather", &evict_gather);
+  m.def("evict", &evict);
 }
