@@ -70,12 +70,12 @@ int launch(const CUtensorMap& mq, const mala::KeyMassParams& p, unsigned grid, c
   return MALA_OK;
 }
 
-template <int D, int kCols>
+template <int D, int kCols, int kBlocks>
 int launch_window(const CUtensorMap& mq, const CUtensorMap& mk, mala::WinParams wp, cudaStream_t st) {
-  using Lay = mala::WinLayout<D, kCols>;
-  wp.k_stages = std::min(Lay::MAX_STAGES, (232448 - Lay::bytes(wp.col_blocks, 0)) / Lay::K_BYTES);
-  const int bytes = Lay::bytes(wp.col_blocks, wp.k_stages);
-  auto kern = mala::mala_key_mass_window_kernel<D, kCols>;
+  using Lay = mala::WinLayout<D, kCols, kBlocks>;
+  wp.k_stages = std::min(Lay::MAX_STAGES, (232448 - Lay::bytes(0)) / Lay::K_BYTES);
+  const int bytes = Lay::bytes(wp.k_stages);
+  auto kern = mala::mala_key_mass_window_kernel<D, kCols, kBlocks>;
   if (set_smem(kern, bytes) != MALA_OK) return MALA_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(wp.m.B) * wp.m.Hkv * wp.parts;
   kern<<<grid, Lay::THREADS, bytes, st>>>(mq, mk, wp);
@@ -89,8 +89,6 @@ int run_window(const void* q, const void* k, const mala::KeyMassParams& p, int c
   mala::WinParams wp = {};
   wp.m = p;
   wp.rows_pad = cols / p.G;
-  wp.col_blocks = cols > 256 ? 2 : 1;
-  const int block = ((cols + wp.col_blocks - 1) / wp.col_blocks + 63) & ~63;
   // CTAs per (b, KV head): the count whose waves of one CTA per SM take the fewest key tiles in all
   const long long units = static_cast<long long>(p.B) * p.Hkv, tiles = (p.Lk + 127) / 128;
   const long long sms = sm_count();
@@ -106,12 +104,12 @@ int run_window(const void* q, const void* k, const mala::KeyMassParams& p, int c
   CUtensorMap mq, mk;
   if (!make_bshd_map(&mq, q, tb, tq, p.Hq, D, wp.rows_pad) || !make_bshd_map(&mk, k, tb, tk, p.Hkv, D, 128))
     return MALA_ERR_CUDA;
-  switch (block) {
-    case 64: return launch_window<D, 64>(mq, mk, wp, st);
-    case 128: return launch_window<D, 128>(mq, mk, wp, st);
-    case 192: return launch_window<D, 192>(mq, mk, wp, st);
-    default: return launch_window<D, 256>(mq, mk, wp, st);
-  }
+  if (cols > 384) return launch_window<D, 256, 2>(mq, mk, wp, st);
+  if (cols > 256) return launch_window<D, 192, 2>(mq, mk, wp, st);
+  if (cols > 192) return launch_window<D, 256, 1>(mq, mk, wp, st);
+  if (cols > 128) return launch_window<D, 192, 1>(mq, mk, wp, st);
+  if (cols > 64) return launch_window<D, 128, 1>(mq, mk, wp, st);
+  return launch_window<D, 64, 1>(mq, mk, wp, st);
 }
 
 int check(int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale, int window, float decay, int ld) {

@@ -8,9 +8,11 @@
 // tile costs its K and one MMA of N = kCols columns per half-row step, and no
 // start-up per key block (walks as in mala_key_mass_kernel took 174 us for the
 // case below, most of it the walks' starts).
-//   warps 0-15  compute: warp w owns the keys 32 (w % 4) .. + 31 of a tile and the
-//               columns (w / 4) kCols / 4 .. of a block; the four column groups'
-//               sums meet in shared memory, and group 0 writes the result
+//   warps 0-15  compute. Up to 256 columns (one block): two teams of eight warps take
+//               the tiles in turn, a warp 32 keys and half of the columns, so that one
+//               team's waits are filled by the other's exponentials. Two blocks: all
+//               sixteen on a tile, a warp a quarter of each block. The parts' sums
+//               meet in shared memory, and the first part's warps write the result
 //   warp  16    producer: Q once, K tiles through a ring
 //   warp  17    MMA issuer (one thread): S^T = K Q^T, two TMEM buffers in turn
 // Columns past a head's rows hold zeros in Q and -infinity in place of -LSE, so
@@ -32,41 +34,40 @@ constexpr int kWinPoly = 2;       // of every eight packed pairs, how many go th
 struct WinParams {
   KeyMassParams m;  // n_blocks, n_chunks, chunk_q and part are not used
   int rows_pad;     // W rounded up to 8: a head's columns
-  int col_blocks;   // blocks of kCols columns (1 or 2)
   int parts;        // CTAs per (b, KV head)
   int k_stages;     // K ring
 };
 
-template <int D, int kCols>
+template <int D, int kCols, int kBlocks>
 struct WinLayout {
   static constexpr int THREADS = 18 * 32;
   static constexpr int K_BYTES = 128 * D * 2;
   static constexpr int MAX_STAGES = 4;
-  static constexpr int AHEAD = 6;  // tiles that the earlier masses are fetched ahead (a tile may take 0.3 us)
-  // lse [512], pos [512], red [2][4][128], earlier masses [AHEAD + 1][128], then barriers
+  static constexpr int TEAMS = kBlocks == 1 ? 2 : 1;  // of compute warps, a tile each
+  static constexpr int PARTS = 4 / TEAMS;             // of a block's columns, one to a warp
+  static constexpr int AHEAD = 6 / TEAMS;  // a team's tiles that the earlier masses are fetched ahead (a tile may take 0.3 us)
+  // lse [512], pos [512], red [TEAMS][2][PARTS][128], earlier masses [TEAMS][AHEAD + 1][128], then barriers
   static constexpr int OFF_LSE = 0;
   static constexpr int OFF_POS = OFF_LSE + kWinMaxCols * 4;
   static constexpr int OFF_RED = OFF_POS + kWinMaxCols * 4;
   static constexpr int OFF_OLD = OFF_RED + 2 * 4 * 128 * 4;
-  static constexpr int OFF_BAR = OFF_OLD + (AHEAD + 1) * 128 * 4;
+  static constexpr int OFF_BAR = OFF_OLD + TEAMS * (AHEAD + 1) * 128 * 4;
   // k_full[4], k_empty[4], s_full[2], s_empty[2], q_full, q_ready, mma_final
   static constexpr int N_BARS = 2 * MAX_STAGES + 4 + 3;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int OFF_Q = (OFF_MISC + 16 + 1023) & ~1023;
-  static constexpr int q_bytes(int col_blocks) { return col_blocks * kCols * D * 2; }
-  static constexpr int bytes(int col_blocks, int stages) {
-    return OFF_Q + q_bytes(col_blocks) + stages * K_BYTES + 1024;
-  }
+  static constexpr int bytes(int stages) { return OFF_Q + kBlocks * kCols * D * 2 + stages * K_BYTES + 1024; }
 };
 
-template <int D, int kCols>
-__global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
+template <int D, int kCols, int kBlocks>
+__global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
     mala_key_mass_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                                 const WinParams wp) {
-  using Lay = WinLayout<D, kCols>;
+  using Lay = WinLayout<D, kCols, kBlocks>;
   const KeyMassParams& p = wp.m;
   constexpr uint32_t IDESC = idesc_bf16(128, kCols, false, false);
-  constexpr int CG = kCols / 4;  // columns of a block per compute warp
+  constexpr int TEAMS = Lay::TEAMS, PARTS = Lay::PARTS;
+  constexpr int CG = kCols / PARTS;  // columns of a block per compute warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sLse = reinterpret_cast<float*>(smem + Lay::OFF_LSE);
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint8_t* sQ = smem + Lay::OFF_Q;
-  const int cols = wp.col_blocks * kCols;  // columns in all
+  constexpr int cols = kBlocks * kCols;  // columns in all
   uint8_t* sK = sQ + cols * D * 2;
   const int NK = wp.k_stages;
 
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 16);
+      mbar_init(&s_empty[i], 16 / TEAMS);
     }
     mbar_init(q_full, 1);
     mbar_init(q_ready, 16);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
         // loop), so the bounded wait expires and the CTA takes its abort path
         if (t == p.stall_tile && !mbar_wait(mma_final, 0, fs)) break;
         if (!mbar_wait(&k_full[st], par, fs)) break;
-        for (int y = 0; y < wp.col_blocks; ++y, ++n) {
+        for (int y = 0; y < kBlocks; ++y, ++n) {
           if (n >= 2 && !mbar_wait(&s_empty[n & 1], ((n >> 1) - 1) & 1, fs)) {
             ok = false;
             break;
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ compute warps
-    const int wq = warp & 3, cg = warp >> 2;
+    const int wq = warp & 3, cg = (warp >> 2) % PARTS, team = warp / (16 / TEAMS);
     const int tid = wq * 32 + lane;  // key within the tile
     bool aborted = !mbar_wait_warp(q_full, 0, fs);
     // rows that do not count: of a head past its rows (another sequence's, perhaps), and past the last head
@@ -231,17 +232,17 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
     const uint32_t lse_a = smem_u32(sLse) + cg * CG * 4;
     const int p_min = sq.P0 + sq.first;  // position of the first row that counts
-    // Group 0 adds the earlier masses: each thread copies its key's into its own slot of a ring
-    // in shared memory, AHEAD tiles before it reads it. A sequence's own tokens start from 0.
+    // The warps of the first columns add the earlier masses: each thread copies its key's into its own
+    // slot of a ring in shared memory, AHEAD tiles before it reads it. A sequence's own tokens start from 0.
     constexpr int AHEAD = Lay::AHEAD;
     const bool has_old = cg == 0 && p.mass_in != nullptr && p.decay != 0.f;
-    float* sOld = reinterpret_cast<float*>(smem + Lay::OFF_OLD) + tid;
+    float* sOld = reinterpret_cast<float*>(smem + Lay::OFF_OLD) + team * (AHEAD + 1) * 128 + tid;
     auto fetch_old = [&](int t, int slot) {
       const int key = (t0 + t) * 128 + tid;
       if (has_old && t < T && key < sq.P0) cp_async_4(smem_u32(sOld + slot * 128), p.mass_in + row_at + key);
       cp_async_commit();  // one group a tile, empty or not, so that the counting holds
     };
-    for (int t = 0; t < AHEAD; ++t) fetch_old(t, t);
+    for (int i = 0; i < AHEAD; ++i) fetch_old(team + i * TEAMS, i);
     int slot = 0;
     // this key's weights summed over the warp's columns of block y, whose scores are in buffer buf;
     // kPlain: every row sees every key of the tile
@@ -295,24 +296,25 @@ __global__ void __launch_bounds__(WinLayout<D, kCols>::THREADS, 1)
       f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
       return lo + hi;
     };
-    int n = 0;
-    for (int t = 0; t < T; ++t) {
+    int n = team, use = 0;  // (tile, block) pairs, in two buffers in turn; the team's tiles
+    for (int t = team; t < T; t += TEAMS, ++use) {
       const int k0 = (t0 + t) * 128, key = k0 + tid;
       const bool mine = cg == 0 && key < sq.Lk;
-      fetch_old(t + AHEAD, slot == 0 ? AHEAD : slot - 1);
+      fetch_old(t + AHEAD * TEAMS, slot == 0 ? AHEAD : slot - 1);
       const bool plain = k0 + 127 <= p_min;  // every row sees every key
       float sum = 0.f;
-      for (int y = 0; y < wp.col_blocks; ++y, ++n) {
+      for (int y = 0; y < kBlocks; ++y, n += TEAMS) {
         if (!aborted) aborted = !mbar_wait_warp(&s_full[n & 1], (n >> 1) & 1, fs);
         if (aborted) continue;  // the barriers below are still met
         tc_fence_after();
         sum += plain ? strip(std::true_type(), n & 1, y, key) : strip(std::false_type(), n & 1, y, key);
       }
-      float* red = sRed + (t & 1) * 512;
-      red[cg * 128 + tid] = sum;
-      named_bar_sync(1, 512);  // the next tile writes the other half of sRed
+      float* red = sRed + (team * 2 + (use & 1)) * (PARTS * 128) + tid;
+      red[cg * 128] = sum;
+      named_bar_sync(1 + team, 512 / TEAMS);  // the team's next tile writes the other half of red
       if (mine && !aborted && !abort_raised(fs)) {
-        float m = (red[tid] + red[128 + tid]) + (red[256 + tid] + red[384 + tid]);
+        float m = red[0] + red[128];
+        if constexpr (PARTS == 4) m += red[256] + red[384];
         cp_async_wait<AHEAD>();
         if (has_old && key < sq.P0) m = fmaf(p.decay, sOld[slot * 128], m);
         p.mass_out[row_at + key] = m;
