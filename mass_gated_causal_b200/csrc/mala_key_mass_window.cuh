@@ -8,20 +8,21 @@
 // tile costs its K and one MMA of N = kCols columns per half-row step, and no
 // start-up per key block (walks as in mala_key_mass_kernel took 174 us for the
 // case below, most of it the walks' starts).
-//   warps 0-15  compute. Up to 256 columns (one block): two teams of eight warps take
-//               the tiles in turn, a warp 32 keys and half of the columns, so that one
-//               team's waits are filled by the other's exponentials. Two blocks: all
-//               sixteen on a tile, a warp a quarter of each block. The parts' sums
-//               meet in shared memory, and the first part's warps write the result
+//   warps 0-15  compute, two teams of eight that do not wait for each other's tiles, so
+//               that one's waits are filled by the other's exponentials: up to 256
+//               columns (one block) they take the tiles in turn, else a block each of
+//               every tile. A warp has 32 keys and half of the block's columns; the
+//               parts' sums meet in shared memory, and the first part's warps write
+//               the result
 //   warp  16    producer: Q once, K tiles through a ring
 //   warp  17    MMA issuer (one thread): S^T = K Q^T, two TMEM buffers in turn
 // Columns past a head's rows hold zeros in Q and -infinity in place of -LSE, so
 // they add nothing (at most 2^-126). Bound: G x W exponentials per key on the
 // special-function unit (at 256 columns 2,048 cycles a tile against 760 for reading
 // K at the HBM rate), a quarter of them moved to the FMA pipes (exp2_poly2). 64 rows
-// of 32 heads over 8 KV heads against 2 x 32,000 keys: 51 us (53 with an eighth, 56
-// with none, 51 with three eighths); one row, which only reads K, 33 us, of which
-// 21 are K's bytes.
+// of 32 heads over 8 KV heads against 2 x 32,000 keys: 45 us (47 with an eighth on the
+// FMA pipes, 46 with three eighths; 51.5 with all sixteen warps on one tile); one row,
+// which only reads K, 28 us, of which 21 are K's bytes.
 #pragma once
 
 #include "mala_key_mass.cuh"
@@ -43,15 +44,14 @@ struct WinLayout {
   static constexpr int THREADS = 18 * 32;
   static constexpr int K_BYTES = 128 * D * 2;
   static constexpr int MAX_STAGES = 4;
-  static constexpr int TEAMS = kBlocks == 1 ? 2 : 1;  // of compute warps, a tile each
-  static constexpr int PARTS = 4 / TEAMS;             // of a block's columns, one to a warp
-  static constexpr int AHEAD = 6 / TEAMS;  // a team's tiles that the earlier masses are fetched ahead (a tile may take 0.3 us)
-  // lse [512], pos [512], red [TEAMS][2][PARTS][128], earlier masses [TEAMS][AHEAD + 1][128], then barriers
+  static constexpr int STEP = kBlocks == 1 ? 2 : 1;  // between a team's tiles
+  static constexpr int AHEAD = 6 / STEP;  // a team's tiles that the earlier masses are fetched ahead (a tile may take 0.3 us)
+  // lse [512], pos [512], sums [2][4][128], earlier masses [STEP][AHEAD + 1][128], then barriers
   static constexpr int OFF_LSE = 0;
   static constexpr int OFF_POS = OFF_LSE + kWinMaxCols * 4;
   static constexpr int OFF_RED = OFF_POS + kWinMaxCols * 4;
   static constexpr int OFF_OLD = OFF_RED + 2 * 4 * 128 * 4;
-  static constexpr int OFF_BAR = OFF_OLD + TEAMS * (AHEAD + 1) * 128 * 4;
+  static constexpr int OFF_BAR = OFF_OLD + STEP * (AHEAD + 1) * 128 * 4;
   // k_full[4], k_empty[4], s_full[2], s_empty[2], q_full, q_ready, mma_final
   static constexpr int N_BARS = 2 * MAX_STAGES + 4 + 3;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
   using Lay = WinLayout<D, kCols, kBlocks>;
   const KeyMassParams& p = wp.m;
   constexpr uint32_t IDESC = idesc_bf16(128, kCols, false, false);
-  constexpr int TEAMS = Lay::TEAMS, PARTS = Lay::PARTS;
-  constexpr int CG = kCols / PARTS;  // columns of a block per compute warp
+  constexpr int STEP = Lay::STEP;
+  constexpr int CG = kCols / 2;  // columns per compute warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sLse = reinterpret_cast<float*>(smem + Lay::OFF_LSE);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 16 / TEAMS);
+      mbar_init(&s_empty[i], 8);
     }
     mbar_init(q_full, 1);
     mbar_init(q_ready, 16);
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ compute warps
-    const int wq = warp & 3, cg = (warp >> 2) % PARTS, team = warp / (16 / TEAMS);
+    const int wq = warp & 3, cg = (warp >> 2) & 1, team = warp >> 3;
+    const int y = kBlocks == 1 ? 0 : team;  // this warp's block
     const int tid = wq * 32 + lane;  // key within the tile
     bool aborted = !mbar_wait_warp(q_full, 0, fs);
     // rows that do not count: of a head past its rows (another sequence's, perhaps), and past the last head
@@ -230,26 +231,27 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
 
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
-    const uint32_t lse_a = smem_u32(sLse) + cg * CG * 4;
+    const uint32_t tS = tmem + team * 256 + cg * CG + lane_base;  // each team has its own buffer of scores
+    const uint32_t la = smem_u32(sLse) + (y * kCols + cg * CG) * 4;
+    const int* pos_a = sPos + y * kCols + cg * CG;
     const int p_min = sq.P0 + sq.first;  // position of the first row that counts
     // The warps of the first columns add the earlier masses: each thread copies its key's into its own
     // slot of a ring in shared memory, AHEAD tiles before it reads it. A sequence's own tokens start from 0.
     constexpr int AHEAD = Lay::AHEAD;
-    const bool has_old = cg == 0 && p.mass_in != nullptr && p.decay != 0.f;
-    float* sOld = reinterpret_cast<float*>(smem + Lay::OFF_OLD) + team * (AHEAD + 1) * 128 + tid;
+    const bool first = cg == 0 && y == 0;
+    const bool has_old = first && p.mass_in != nullptr && p.decay != 0.f;
+    float* sOld = reinterpret_cast<float*>(smem + Lay::OFF_OLD) + (STEP == 2 ? team * (AHEAD + 1) * 128 : 0) + tid;
     auto fetch_old = [&](int t, int slot) {
       const int key = (t0 + t) * 128 + tid;
       if (has_old && t < T && key < sq.P0) cp_async_4(smem_u32(sOld + slot * 128), p.mass_in + row_at + key);
       cp_async_commit();  // one group a tile, empty or not, so that the counting holds
     };
-    for (int i = 0; i < AHEAD; ++i) fetch_old(team + i * TEAMS, i);
+    const int t_first = STEP == 2 ? team : 0;  // the team's first tile
+    for (int i = 0; i < AHEAD; ++i) fetch_old(t_first + i * STEP, i);
     int slot = 0;
-    // this key's weights summed over the warp's columns of block y, whose scores are in buffer buf;
-    // kPlain: every row sees every key of the tile
-    auto strip = [&](auto plain_c, int buf, int y, int key) -> float {
+    // this key's weights summed over the warp's columns; kPlain: every row sees every key of the tile
+    auto strip = [&](auto plain_c, int key) -> float {
       constexpr bool kPlain = decltype(plain_c)::value;
-      const uint32_t tS = tmem + buf * 256 + cg * CG + lane_base;
-      const uint32_t la = lse_a + y * kCols * 4;
       uint64_t acc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
         if (c0 == kLast) {  // the block is out of TMEM: its columns go back to the MMA issuer
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[buf]);
+          if (lane == 0) mbar_arrive(&s_empty[team]);
         }
 #pragma unroll
         for (int j = 0; j < 32 && c0 + j < CG; j += 16) {
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
-          const int* pos = sPos + y * kCols + cg * CG + c0 + j;
+          const int* pos = pos_a + c0 + j;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (kPlain && e % 2 == 1 && e < 2 * kWinPoly) {
@@ -296,29 +298,36 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
       f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
       return lo + hi;
     };
-    int n = team, use = 0;  // (tile, block) pairs, in two buffers in turn; the team's tiles
-    for (int t = team; t < T; t += TEAMS, ++use) {
+    int use = 0;  // of the team's buffer
+    for (int t = t_first; t < T; t += STEP, ++use) {
       const int k0 = (t0 + t) * 128, key = k0 + tid;
-      const bool mine = cg == 0 && key < sq.Lk;
-      fetch_old(t + AHEAD * TEAMS, slot == 0 ? AHEAD : slot - 1);
-      const bool plain = k0 + 127 <= p_min;  // every row sees every key
+      fetch_old(t + AHEAD * STEP, slot == 0 ? AHEAD : slot - 1);
       float sum = 0.f;
-      for (int y = 0; y < kBlocks; ++y, n += TEAMS) {
-        if (!aborted) aborted = !mbar_wait_warp(&s_full[n & 1], (n >> 1) & 1, fs);
-        if (aborted) continue;  // the barriers below are still met
+      if (!aborted) aborted = !mbar_wait_warp(&s_full[team], use & 1, fs);
+      if (!aborted) {  // (the barriers below are met in any case)
         tc_fence_after();
-        sum += plain ? strip(std::true_type(), n & 1, y, key) : strip(std::false_type(), n & 1, y, key);
+        sum = k0 + 127 <= p_min ? strip(std::true_type(), key) : strip(std::false_type(), key);
       }
-      float* red = sRed + (team * 2 + (use & 1)) * (PARTS * 128) + tid;
-      red[cg * 128] = sum;
-      named_bar_sync(1 + team, 512 / TEAMS);  // the team's next tile writes the other half of red
-      if (mine && !aborted && !abort_raised(fs)) {
+      // Where the parts' sums meet: one block, both halves of the team's tile; two, those of the second
+      // team too, which runs up to two tiles ahead of the first.
+      float* red = sRed + (kBlocks == 1 ? team * 2 + (use & 1) : 2 * (use & 1)) * 256 + tid;
+      if (kBlocks == 1) {
+        red[cg * 128] = sum;
+        named_bar_sync(1 + team, 256);  // the team's next tile writes the other half of red
+      } else {
+        if (team == 1 && use >= 2) named_bar_sync(3 + (use & 1), 512);  // the first team has read
+        red[(2 * y + cg) * 128] = sum;
+        if (team == 1) named_bar_arrive(1 + (use & 1), 512);
+        else named_bar_sync(1 + (use & 1), 512);
+      }
+      if (first && key < sq.Lk && !aborted && !abort_raised(fs)) {
         float m = red[0] + red[128];
-        if constexpr (PARTS == 4) m += red[256] + red[384];
+        if constexpr (kBlocks == 2) m += red[256] + red[384];
         cp_async_wait<AHEAD>();
         if (has_old && key < sq.P0) m = fmaf(p.decay, sOld[slot * 128], m);
         p.mass_out[row_at + key] = m;
       }
+      if (kBlocks == 2 && team == 0 && t + 2 < T) named_bar_arrive(3 + (use & 1), 512);
       slot = slot == AHEAD ? 0 : slot + 1;
     }
   }

@@ -257,3 +257,25 @@ def test_binding_checks(cuda_lib):
             cuda_lib.key_mass(**a)
     with pytest.raises(cuda_lib.MalaError):
         cuda_lib.key_mass(q, k, lse, 0.1, out=torch.zeros(1, 2, 29, device="cuda"))
+
+
+@pytest.mark.parametrize("Lq,tile,reached", [(100, 0, True), (100, 1, True), (60, 1, True), (100, 2000, False)])
+def test_teams_that_wait_in_vain_end(cuda_lib, Lq, tile, reached):
+    """Few rows, the keys streaming past them: two blocks of columns (416) and one (256), a team of warps each."""
+    q, k = inputs(1, 4, 1, Lq, 9000, 64, seed=1)
+    lse = lse_of(q, k, 0.1)
+    want = cuda_lib.key_mass(q, k, lse, 0.1, mass=torch.ones(1, 1, 9000, device="cuda"), decay=0.5)
+    cuda_lib.mala_test_hooks(20_000_000, tile, None)
+    try:
+        cuda_lib.key_mass(q, k, lse, 0.1)
+        # 71 key tiles go to a CTA each; of eight heads, several to a CTA
+        q2, k2 = (x.repeat(1, 1, 8, 1) for x in (q, k))
+        cuda_lib.key_mass(q2, k2, lse.repeat(1, 8, 1), 0.1)
+        assert cuda_lib.mala_check_status() == (cuda_lib.MALA_ERR_DEVICE_TIMEOUT if reached else 0)
+    finally:
+        cuda_lib.mala_test_hooks(0, -1, None)
+    got = cuda_lib.key_mass(q, k, lse, 0.1, mass=torch.ones(1, 1, 9000, device="cuda"), decay=0.5)
+    assert cuda_lib.mala_check_status() == 0 and torch.equal(got, want)
+    many = cuda_lib.key_mass(q2, k2, lse.repeat(1, 8, 1), 0.1)
+    for h in range(8):
+        torch.testing.assert_close(many[:, h], cuda_lib.key_mass(q, k, lse, 0.1)[:, 0], rtol=2.0 ** -20, atol=0)
