@@ -212,6 +212,24 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
     return;
   }
 
+  constexpr int W = D / 4;  // 32-bit words of half a row of K
+  uint32_t w[32];           // compute warps: half of this key's row, on its way while the CTA sets up
+  if (warp < CW && key < sq.Lk) {
+    const size_t row = p.cu_q != nullptr ? static_cast<size_t>(sq.k_off) + key : static_cast<size_t>(b) * sq.Lk + key;
+    const uint4* src = reinterpret_cast<const uint4*>(p.k + (row * p.Hkv + hkv) * D + half * (D / 2));
+#pragma unroll
+    for (int e = 0; e < W / 4; ++e) {
+      const uint4 v = __ldg(src + e);
+      w[4 * e] = v.x;
+      w[4 * e + 1] = v.y;
+      w[4 * e + 2] = v.z;
+      w[4 * e + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e) w[e] = 0u;
+  }
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < NQ; ++i) {
       mbar_init(&q_full[i], 2);
@@ -316,25 +334,7 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
     // ------------------------------------------------------------ compute warps
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     {  // half of this key's row into tensor memory (A operand: two values to a column)
-      constexpr int W = D / 4;  // 32-bit words of half a row
       const uint32_t tK = tmem + Lay::COL_K + x * (D / 2) + half * W + lane_base;
-      uint32_t w[32];
-      if (key < sq.Lk) {
-        const size_t row = p.cu_q != nullptr ? static_cast<size_t>(sq.k_off) + key
-                                             : static_cast<size_t>(b) * sq.Lk + key;
-        const uint4* src = reinterpret_cast<const uint4*>(p.k + (row * p.Hkv + hkv) * D + half * (D / 2));
-#pragma unroll
-        for (int e = 0; e < W / 4; ++e) {
-          const uint4 v = __ldg(src + e);
-          w[4 * e] = v.x;
-          w[4 * e + 1] = v.y;
-          w[4 * e + 2] = v.z;
-          w[4 * e + 3] = v.w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = 0u;
-      }
       __syncwarp();
       if constexpr (W == 32) tmem_st32(tK, w);
       else tmem_st16(tK, *reinterpret_cast<uint32_t(*)[16]>(w));
