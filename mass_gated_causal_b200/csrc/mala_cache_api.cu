@@ -96,13 +96,18 @@ int launch_rope(mala::RopeParams p, int d, bool adjacent, cudaStream_t st) {
 // ------------------------------------------------------------------ evict
 template <int C, int kKeep>
 int launch_select_keep(const mala::EvictParams& p, cudaStream_t st) {
+  auto kern = mala::mala_evict_select_kernel<C, kKeep>;
+  constexpr int kBytes = kKeep * mala::kEvictThreads * 4;
+  // (beside the 24 KB of counts it passes the 48 KB that need no leave)
+  if (kBytes > 20 * 1024 && set_smem(kern, kBytes) != MALA_OK) return MALA_ERR_CUDA;
   if constexpr (C == 1) {
-    mala::mala_evict_select_kernel<C, kKeep><<<static_cast<unsigned>(p.B) * p.Hkv, mala::kEvictThreads, 0, st>>>(p);
+    kern<<<static_cast<unsigned>(p.B) * p.Hkv, mala::kEvictThreads, kBytes, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * C);
   cfg.blockDim = dim3(mala::kEvictThreads);
+  cfg.dynamicSmemBytes = kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -110,7 +115,7 @@ int launch_select_keep(const mala::EvictParams& p, cudaStream_t st) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, mala::mala_evict_select_kernel<C, kKeep>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
     cudaGetLastError();
     return MALA_ERR_CUDA;
   }
@@ -121,8 +126,12 @@ template <int C>
 int launch_select(const mala::EvictParams& p, cudaStream_t st) {
   // masses a thread meets in the longest row
   const int each = (p.ld + C * mala::kEvictThreads - 1) / (C * mala::kEvictThreads);
+  // (keys kept for 1, 4, 16 or 32 of them: 1K rows of masses 3.7 us with one, 4.0 with room for four;
+  // 64 rows of 64K masses 18.4 us with 32, 48 with every pass reading the masses again)
+  if (each <= 1) return launch_select_keep<C, 1>(p, st);
   if (each <= 4) return launch_select_keep<C, 4>(p, st);
   if (each <= 16) return launch_select_keep<C, 16>(p, st);
+  if (each <= 32) return launch_select_keep<C, 32>(p, st);
   return launch_select_keep<C, 0>(p, st);
 }
 

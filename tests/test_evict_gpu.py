@@ -205,3 +205,21 @@ def test_binding_checks(cuda_lib):
         cuda_lib.evict_gather(index, new, k, v, t[:1], t)
     with pytest.raises(ValueError):
         cuda_lib.evict_gather(index[:, :2].contiguous(), new, k, v, t, t)
+
+
+@pytest.mark.parametrize("kind", ["spread", "few", "equal", "nan"])
+@pytest.mark.parametrize("n,ld", [(1, 1024), (3, 1025), (3, 3900), (2, 33000), (80, 15000), (80, 32700), (80, 32800), (40, 66000)])
+def test_select_at_every_length_of_a_thread(cuda_lib, kind, n, ld):
+    """Rows that leave a thread one mass, a few, up to 32 and more, by one CTA and by clusters; lengths beside warps' ends."""
+    g = torch.Generator(device="cuda").manual_seed(ld)
+    m = torch.rand(n, 1, ld, generator=g, device="cuda")
+    if kind == "spread":
+        m = 1.0 / (m + 1e-4)
+    elif kind == "few":
+        m = (m * 3).floor() - 1.0
+    elif kind == "equal":
+        m.fill_(2.0)
+    else:
+        m[m < 0.99] = float("nan")
+    lens = [ld, ld - 1, ld - 33][:n] + [ld - 31 * i for i in range(3, n)]
+    check_select(cuda_lib, m, lens, ld // 5, 3, 40)
