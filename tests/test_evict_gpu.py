@@ -208,7 +208,8 @@ def test_binding_checks(cuda_lib):
 
 
 @pytest.mark.parametrize("kind", ["spread", "few", "equal", "nan"])
-@pytest.mark.parametrize("n,ld", [(1, 1024), (3, 1025), (3, 3900), (2, 33000), (80, 15000), (80, 32700), (80, 32800), (40, 66000)])
+@pytest.mark.parametrize("n,ld", [(1, 1024), (3, 1025), (3, 3900), (2, 33000), (2, 200000), (20, 100000), (40, 60000),
+                                  (80, 15000), (80, 32700), (80, 32800), (40, 66000)])
 def test_select_at_every_length_of_a_thread(cuda_lib, kind, n, ld):
     """Rows that leave a thread one mass, a few, up to 32 and more, by one CTA and by clusters; lengths beside warps' ends."""
     g = torch.Generator(device="cuda").manual_seed(ld)
