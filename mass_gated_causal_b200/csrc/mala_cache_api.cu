@@ -320,9 +320,8 @@ int mala_evict_gather(const void* k_pages, const void* v_pages, const int32_t* b
   if (gx >= (1ll << 31)) return MALA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(B));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d == 128) mala::mala_evict_gather_kernel<128><<<grid, mala::kGatherThreads, 0, st>>>(p);
-  else mala::mala_evict_gather_kernel<64><<<grid, mala::kGatherThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
+  auto kern = d == 128 ? mala::mala_evict_gather_kernel<128> : mala::mala_evict_gather_kernel<64>;
+  return launch_second(kern, grid, mala::kGatherThreads, st, p);  // usually mala_evict_select's second half
 }
 
 }  // extern "C"

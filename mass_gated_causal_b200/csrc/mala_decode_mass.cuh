@@ -74,6 +74,7 @@ __device__ __forceinline__ float merged_lse(const float* lp, int n, int lane, fl
 // GP: the group's heads rounded up to 1, 2, 4 or 8 (scores a thread holds at once).
 template <int D, int GP>
 __global__ void __launch_bounds__(kDecMassThreads) mala_decode_mass_kernel(const DecMassParams p) {
+  cudaGridDependencySynchronize();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) < p.merge_blocks) {
     const int row = blockIdx.x * (kDecMassThreads / 32) + warp;

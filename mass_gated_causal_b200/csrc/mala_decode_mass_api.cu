@@ -94,11 +94,11 @@ int launch_short(const CUtensorMap& mk, const CUtensorMap& mv, mala::FlatParams 
 
 template <int D>
 int launch_mass(const mala::DecMassParams& m, unsigned grid, cudaStream_t st) {
-  if (m.G <= 1) mala::mala_decode_mass_kernel<D, 1><<<grid, mala::kDecMassThreads, 0, st>>>(m);
-  else if (m.G <= 2) mala::mala_decode_mass_kernel<D, 2><<<grid, mala::kDecMassThreads, 0, st>>>(m);
-  else if (m.G <= 4) mala::mala_decode_mass_kernel<D, 4><<<grid, mala::kDecMassThreads, 0, st>>>(m);
-  else mala::mala_decode_mass_kernel<D, 8><<<grid, mala::kDecMassThreads, 0, st>>>(m);
-  return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
+  auto kern = m.G <= 1   ? mala::mala_decode_mass_kernel<D, 1>
+              : m.G <= 2 ? mala::mala_decode_mass_kernel<D, 2>
+              : m.G <= 4 ? mala::mala_decode_mass_kernel<D, 4>
+                         : mala::mala_decode_mass_kernel<D, 8>;
+  return launch_second(kern, dim3(grid), mala::kDecMassThreads, st, m);
 }
 
 template <int D, int BK, int GP>

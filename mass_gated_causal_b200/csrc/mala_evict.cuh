@@ -310,6 +310,7 @@ constexpr int kGatherRows = 4;  // rows of a head a thread copies 16 bytes of, K
 
 template <int D>
 __global__ void __launch_bounds__(kGatherThreads) mala_evict_gather_kernel(const GatherParams p) {
+  cudaGridDependencySynchronize();
   constexpr int LPR = D / 8, SLOTS = kGatherThreads / LPR;
   const int b = blockIdx.y;
   const int len = min(__ldg(p.lens + b), p.budget);

@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
 // (A template so that more than one translation unit may include this file.)
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) mala_key_mass_join_kernel(const KeyMassParams p) {
+  cudaGridDependencySynchronize();
   const int bk = blockIdx.y, b = bk / p.Hkv;
   const int key = blockIdx.x * kThreads + threadIdx.x;
   const KeyMassSeq sq = key_mass_seq(p, b);

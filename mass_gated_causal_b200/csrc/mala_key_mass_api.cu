@@ -64,8 +64,7 @@ int launch(const CUtensorMap& mq, const mala::KeyMassParams& p, unsigned grid, c
   if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
   if (p.n_chunks > 1) {
     const dim3 jg(static_cast<unsigned>((p.ld + 255) / 256), static_cast<unsigned>(p.B) * p.Hkv);
-    mala::mala_key_mass_join_kernel<256><<<jg, 256, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return MALA_ERR_CUDA;
+    return launch_second(mala::mala_key_mass_join_kernel<256>, jg, 256, st, p);
   }
   return MALA_OK;
 }

@@ -224,3 +224,44 @@ def test_select_at_every_length_of_a_thread(cuda_lib, kind, n, ld):
         m[m < 0.99] = float("nan")
     lens = [ld, ld - 1, ld - 33][:n] + [ld - 31 * i for i in range(3, n)]
     check_select(cuda_lib, m, lens, ld // 5, 3, 40)
+
+
+def test_gather_captured_behind_a_join(cuda_lib):
+    """The copy alone in a captured graph, behind work of two streams that both write what it reads, and behind a copy."""
+    k, v = pools(24, 64, 2, 64, seed=3)
+    table = torch.randperm(24, device="cuda")[:8].to(torch.int32).view(2, 4)
+    to = torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3)
+    index = torch.zeros(2, 2, 150, dtype=torch.int32, device="cuda")
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    rows = torch.stack([torch.randperm(256, device="cuda")[:150].sort()[0] for _ in range(4)]).view(2, 2, 150)
+    rows = rows.to(torch.int32)
+    ko, vo = torch.zeros(2, 6, 64, 2, 64, dtype=torch.bfloat16, device="cuda").unbind()
+    out = (torch.zeros_like(ko), torch.zeros_like(vo))
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            new.fill_(150)
+        index.add_(rows)
+        torch.cuda.current_stream().wait_stream(side)
+        cuda_lib.evict_gather(index, new, k, v, table, to, ko, vo)
+        out[0].copy_(ko)
+        new.mul_(1)
+        cuda_lib.evict_gather(index, new, k, v, table, to, ko, vo)
+        out[1].copy_(vo)
+        index.zero_()
+        new.zero_()
+    for _ in range(3):
+        ko.zero_()
+        vo.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for pool, got in ((k, out[0]), (v, out[1])):
+            for b in range(2):
+                old = pool[table[b].long()].flatten(0, 1)
+                fresh = got[to[b].long()].flatten(0, 1)
+                for h in range(2):
+                    want = old[rows[b, h].long(), h]
+                    assert torch.equal(fresh[:150, h].view(torch.int16), want.view(torch.int16))
+    assert cuda_lib.mala_check_status() == 0
