@@ -480,8 +480,9 @@ MALA_API size_t mala_key_mass_varlen_workspace_size(int num_seqs, int Hq, int Hk
  * that count: the last `window` of the Lq (0, or at least Lq: all). Keys j >=
  * Lk - Lq are the queries' own tokens and start from 0 (mass_in is not read
  * there). The weights are those of every visible key, whatever tiles a gate
- * (tau > 0) skipped; with tau = 0 each row's weights sum to 1. The sums are
- * fp32, in an order that does not depend on the schedule.
+ * (tau > 0) skipped; with tau = 0 each row's weights sum to 1. The scores are
+ * the tensor cores' fp32 sums, as in mala_fwd. The masses' sums are fp32, in an
+ * order that does not depend on the schedule.
  *
  *   q [B, Lq, Hq, d], k [B, Lk, Hkv, d] bf16, lse [B, Hq, Lq] fp32, in (finite;
  *              a row whose LSE is +infinity adds nothing)

@@ -149,14 +149,14 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   p.cu_k = cu_k;
   p.total_q = total_q;
   p.total_k = total_k;
-  // The tensor core's fp32 accumulator drops bits: a score comes out too small by
-  // about half a step for each of its d / 16 additions. Measured against 64 bits on
-  // random prompts the weights were 1.1e-6 (d = 128) and 2.6e-7 (d = 64) too small
-  // on average; the factor below takes that back (2e-7 and 1e-7 are left, the scores
-  // scatter). The LSE gets the factor that rounding scale_log2 gave the scores.
-  const double grown = static_cast<double>(scale) * (1.0 + (d == 128 ? 1.5e-7 : 7e-8));
-  p.scale_log2 = static_cast<float>(grown * 1.4426950408889634);
-  const double ratio = p.scale_log2 / grown;
+  // log2(e) as the rounded scale_log2 has it, for the LSE (neg_lse2). The scores stay as the
+  // tensor core sums them, which drops bits: a score comes out up to half a step too small
+  // for each partial sum of its d / 16 (nothing where the partial sums are exact). mala_fwd's
+  // scores lose the same, so beside its LSE nothing is to be taken back: the weights of a row
+  // of 1,500 random keys (d = 128) sum to 1 - 1e-8, and each is within 8e-8 of the softmax;
+  // against an LSE from elsewhere they are 3e-7 too small on average there.
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  const double ratio = p.scale_log2 / static_cast<double>(scale);
   p.lse_hi = static_cast<float>(ratio);
   p.lse_lo = static_cast<float>(ratio - p.lse_hi);
   p.decay = decay;
