@@ -485,7 +485,9 @@ MALA_API size_t mala_key_mass_varlen_workspace_size(int num_seqs, int Hq, int Hk
  * order that does not depend on the schedule.
  *
  *   q [B, Lq, Hq, d], k [B, Lk, Hkv, d] bf16, lse [B, Hq, Lq] fp32, in (finite;
- *              a row whose LSE is +infinity adds nothing)
+ *              a row whose LSE is +infinity adds exactly nothing, and one with a
+ *              NaN, or with a weight past fp32's range, leaves NaN or infinity in
+ *              the mass of every key that it sees)
  *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
  *   mass_out   [B, Hkv, ld_mass] fp32, out; entries j >= Lk become 0. May be
  *              mass_in.

@@ -132,13 +132,15 @@ __device__ __forceinline__ float neg_lse2(const KeyMassParams& p, float lse) {
 // 2^x of a packed pair on the FMA pipes: x = n + f with n the nearest integer,
 // |f| <= 1/2; 2^f by a polynomial of degree 5 (minimax in the relative error, by
 // the Remez exchange: 7.5e-8, with fp32 rounding 2.1e-7, about ex2.approx's own
-// error), n added to the exponent. x is held above -126 (2^-126 counts as
-// nothing); it must stay below 127.
+// error), times 2^n, whose exponent field n + 127 is the low byte of x + kShift.
+// Outside fp32's range as ex2.approx, up to where it ends: 0 below -126.5 (n = -127
+// has the field of zero, so a masked or empty row adds exactly nothing), infinity
+// from 127.5, and NaN stays NaN (the clamps keep it, and so does the product).
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
-  constexpr float kShift = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
+  constexpr float kShift = 12582912.f + 127.f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
   float lo, hi;
   f2_unpack(x, lo, hi);
-  x = f2_pack(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
+  x = f2_pack(clamp_nan(lo, -127.f, 128.f), clamp_nan(hi, -127.f, 128.f));
   const uint64_t m = f2_add(x, f2_pack(kShift, kShift));
   const uint64_t n = f2_add(m, f2_pack(-kShift, -kShift));
   const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), x);
@@ -148,11 +150,9 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
   r = f2_fma(r, f, f2_pack(0.24022120237350464f, 0.24022120237350464f));
   r = f2_fma(r, f, f2_pack(0.6931469440460205f, 0.6931469440460205f));
   r = f2_fma(r, f, f2_pack(1.0000001192092896f, 1.0000001192092896f));
-  float mlo, mhi, rlo, rhi;
+  float mlo, mhi;
   f2_unpack(m, mlo, mhi);
-  f2_unpack(r, rlo, rhi);
-  return f2_pack(__uint_as_float(__float_as_uint(rlo) + (__float_as_uint(mlo) << 23)),
-                 __uint_as_float(__float_as_uint(rhi) + (__float_as_uint(mhi) << 23)));
+  return f2_mul(r, f2_pack(__uint_as_float(__float_as_uint(mlo) << 23), __uint_as_float(__float_as_uint(mhi) << 23)));
 }
 
 constexpr int kMassPoly = 1;  // of every eight packed pairs, how many go through exp2_poly2 (see above)

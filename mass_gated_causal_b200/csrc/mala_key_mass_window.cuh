@@ -17,7 +17,7 @@
 //   warp  16    producer: Q once, K tiles through a ring
 //   warp  17    MMA issuer (one thread): S^T = K Q^T, two TMEM buffers in turn
 // Columns past a head's rows hold zeros in Q and -infinity in place of -LSE, so
-// they add nothing (at most 2^-126). Bound: G x W exponentials per key on the
+// they add nothing. Bound: G x W exponentials per key on the
 // special-function unit (at 256 columns 2,048 cycles a tile against 760 for reading
 // K at the HBM rate), a quarter of them moved to the FMA pipes (exp2_poly2). 64 rows
 // of 32 heads over 8 KV heads against 2 x 32,000 keys: 45 us (47 with an eighth on the

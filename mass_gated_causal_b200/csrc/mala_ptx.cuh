@@ -412,6 +412,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// x held between lo and hi; NaN stays NaN.
+__device__ __forceinline__ float clamp_nan(float x, float lo, float hi) {
+  asm("max.NaN.f32 %0, %0, %1;\n\tmin.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(lo), "f"(hi));
+  return x;
+}
+
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

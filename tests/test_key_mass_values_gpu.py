@@ -60,3 +60,34 @@ def test_weights_of_exact_scores(cuda_lib, Lq, Lk, window, d, where):
     want = 2 * rows * np.exp(352 * scale - lse)
     err = ((got[0] - want).abs() / want).max()
     assert float(err) <= 2.0 ** -21, float(err)
+
+
+@pytest.mark.parametrize("Lq,Lk,window", SHAPES)
+def test_a_row_with_an_infinite_lse_adds_exactly_nothing(cuda_lib, Lq, Lk, window):
+    q, k = alike(Lq, Lk, 64, "all")
+    lse = torch.full((1, 4, Lq), float("inf"), device="cuda")
+    got = cuda_lib.key_mass(q, k, lse, 0.125, window=window)
+    assert cuda_lib.mala_check_status() == 0
+    assert bool((got == 0).all()), float(got.max())
+
+
+@pytest.mark.parametrize("what", ["nan query", "nan lse", "overflow"])
+@pytest.mark.parametrize("Lq,Lk,window", SHAPES)
+def test_a_broken_row_shows_in_every_key_that_it_sees(cuda_lib, Lq, Lk, window, what):
+    """Wherever the row stands among 16 and among the strips: all of its keys' masses are not finite, and no other's."""
+    q, k = alike(Lq, Lk, 64, "all")
+    base = torch.full((1, 4, Lq), 44.0, device="cuda")
+    first = Lq - (window or Lq)
+    for r in list(range(first, min(first + 18, Lq))) + list(range(Lq - 18, Lq)):
+        q2, lse = q.clone(), base.clone()
+        if what == "nan query":
+            q2[0, r, 1] = float("nan")
+        elif what == "nan lse":
+            lse[0, 1, r] = float("nan")
+        else:
+            lse[0, 1, r] = -100.0  # the weight is e^144
+        got = cuda_lib.key_mass(q2, k, lse, 0.125, window=window)
+        seen = torch.arange(Lk, device="cuda") <= r + Lk - Lq
+        assert bool((~got[0, 0].isfinite() == seen).all()), r
+        assert bool(got[0, 1].isfinite().all())
+    assert cuda_lib.mala_check_status() == 0
