@@ -70,7 +70,9 @@ int launch_short(const CUtensorMap& mk, const CUtensorMap& mv, mala::FlatParams 
   p.pitch = Lay::short_pitch(each);
   const int bytes = Lay::short_bytes(p.G, each);
   auto kern = mala::mala_decode_flat_kernel<D, true>;
-  if (set_smem(kern, bytes) != MALA_OK) return MALA_ERR_CUDA;
+  // The limit is the kernel's, shared by all host threads: always the most any call takes, never
+  // this call's size, or another thread's smaller call could lower it between here and the launch.
+  if (set_smem(kern, Lay::short_bytes(kMaxDecodeGroup, mala::kShortTiles)) != MALA_OK) return MALA_ERR_CUDA;
   if (p.cluster > 8 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return MALA_ERR_CUDA;
