@@ -31,6 +31,7 @@
 #pragma once
 
 #include "mala_ptx.cuh"
+#include "mala_short_cluster.h"
 
 namespace mala {
 
@@ -65,8 +66,6 @@ struct FlatParams {
 constexpr int kFlatTile = 64;      // keys per tile
 constexpr int kFlatLeastRun = 2;   // tiles: a run is not cut shorter
 constexpr int kFlatThreads = 160;
-constexpr int kShortTiles = 8;     // kShort: tiles a CTA takes at most
-constexpr int kShortCluster = 16;  // and CTAs of a cluster
 
 template <int D>
 struct FlatLayout {

@@ -1,6 +1,7 @@
 // mala_decode_mass_api.cu -- C ABI of the paged decode that also collects each
 // key's attention weight (host side; the kernels are included below).
 #include <algorithm>
+#include <atomic>
 
 #include "mala_decode.cuh"
 #include "mala_decode_mass.cuh"
@@ -45,22 +46,68 @@ int launch_flat(const CUtensorMap& mk, const CUtensorMap& mv, const mala::FlatPa
   return cudaGetLastError() == cudaSuccess ? MALA_OK : MALA_ERR_CUDA;
 }
 
-// CTAs per (b, KV head) if the whole decode is one launch of clusters, else 0: as
-// many as leave each two tiles and are on the GPU at once. Where even a CTA's eight
-// tiles do not reach the end, or the clusters would come in two waves, equal runs of
-// all tiles are faster: 8 sequences of 2K keys, 8 KV heads, 12.8 us against 16.5 for
-// the two kernels, but 16 of 4K keys in two waves 53 against 46.5.
+// Readies the kernel of short caches for clusters of this size. The limit on shared memory is
+// the kernel's, shared by all host threads: always the most any call takes, never this call's
+// size, or another thread's smaller call could lower it between here and the launch.
 template <int D>
-int short_cluster(long long units, long long keys, int G) {
+int ready_short(int cluster) {
+  auto kern = mala::mala_decode_flat_kernel<D, true>;
+  if (set_smem(kern, mala::FlatLayout<D>::short_bytes(kMaxDecodeGroup, mala::kShortTiles)) != MALA_OK)
+    return MALA_ERR_CUDA;
+  if (cluster > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return MALA_ERR_CUDA;
+  return MALA_OK;
+}
+
+template <int D>
+cudaLaunchConfig_t short_config(unsigned grid, int cluster, int bytes, cudaLaunchAttribute* attr, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(mala::kFlatThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of the short kernel that the current device holds at once (0: none, or the
+// question failed), with two of its CTAs to an SM (`pair`) or one. Asked once per device,
+// for the most shared memory that either takes.
+template <int D>
+int short_room(int cluster, bool pair) {
   using Lay = mala::FlatLayout<D>;
-  const int sms = sm_count();
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][2][5];  // clusters + 1, by log2 of the size
+  int dev = 0, lg = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  while ((1 << lg) < cluster) ++lg;
+  std::atomic<int>* slot = dev < kDevices ? &known[dev][pair ? 1 : 0][lg] : nullptr;
+  if (slot && slot->load() > 0) return slot->load() - 1;
+  cudaLaunchAttribute attr;
+  constexpr int kMost = Lay::short_bytes(kMaxDecodeGroup, mala::kShortTiles);
+  const int bytes = pair ? std::min(Lay::PAIR_BYTES, kMost) : kMost;
+  const cudaLaunchConfig_t cfg = short_config<D>(cluster, cluster, bytes, &attr, nullptr);
+  int n = 0;
+  if (ready_short<D>(cluster) != MALA_OK ||
+      cudaOccupancyMaxActiveClusters(&n, mala::mala_decode_flat_kernel<D, true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (slot) slot->store(n + 1);
+  return n;
+}
+
+template <int D>
+int pick_short(long long units, long long keys, int G) {
+  using Lay = mala::FlatLayout<D>;
   const long long tiles = (keys + mala::kFlatTile - 1) / mala::kFlatTile;
-  int c = 1;
-  while (c < mala::kShortCluster && 2 * c < tiles && units * 2 * c <= 2 * sms) c *= 2;
-  const long long each = (tiles + c - 1) / c;
-  if (each > mala::kShortTiles) return 0;
-  const int resident = Lay::short_bytes(G, static_cast<int>(each)) <= Lay::PAIR_BYTES ? 2 : 1;
-  return units * c <= resident * sms ? c : 0;
+  return mala::short_cluster(units, tiles, 2ll * sm_count(), [&](int c, int each) {
+    return short_room<D>(c, Lay::short_bytes(G, each) <= Lay::PAIR_BYTES);
+  });
 }
 
 template <int D>
@@ -68,26 +115,11 @@ int launch_short(const CUtensorMap& mk, const CUtensorMap& mv, mala::FlatParams 
   using Lay = mala::FlatLayout<D>;
   const int tiles = (p.max_len + mala::kFlatTile - 1) / mala::kFlatTile, each = (tiles + p.cluster - 1) / p.cluster;
   p.pitch = Lay::short_pitch(each);
-  const int bytes = Lay::short_bytes(p.G, each);
-  auto kern = mala::mala_decode_flat_kernel<D, true>;
-  // The limit is the kernel's, shared by all host threads: always the most any call takes, never
-  // this call's size, or another thread's smaller call could lower it between here and the launch.
-  if (set_smem(kern, Lay::short_bytes(kMaxDecodeGroup, mala::kShortTiles)) != MALA_OK) return MALA_ERR_CUDA;
-  if (p.cluster > 8 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return MALA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * p.cluster);
-  cfg.blockDim = dim3(mala::kFlatThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
+  if (ready_short<D>(p.cluster) != MALA_OK) return MALA_ERR_CUDA;
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, mk, mv, p) != cudaSuccess) {
+  const cudaLaunchConfig_t cfg = short_config<D>(static_cast<unsigned>(p.B) * p.Hkv * p.cluster, p.cluster,
+                                                 Lay::short_bytes(p.G, each), &attr, st);
+  if (cudaLaunchKernelEx(&cfg, mala::mala_decode_flat_kernel<D, true>, mk, mv, p) != cudaSuccess) {
     cudaGetLastError();
     return MALA_ERR_CUDA;
   }
@@ -218,7 +250,7 @@ int mala_decode_paged_mass(const void* q, const void* k_pages, const void* v_pag
     p.wait_ns = wait_limit_ns();
     p.stall_tile = stall_tile();
     const long long units = static_cast<long long>(B) * Hkv;
-    p.cluster = d == 128 ? short_cluster<128>(units, max_lk, G) : short_cluster<64>(units, max_lk, G);
+    p.cluster = d == 128 ? pick_short<128>(units, max_lk, G) : pick_short<64>(units, max_lk, G);
     if (p.cluster > 0) {
       p.o = static_cast<uint16_t*>(o);
       p.lse = lse;
