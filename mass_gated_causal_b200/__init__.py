@@ -545,8 +545,9 @@ def _rope_flags(adjacent, cyclic):
 def rope(q, k, v, positions, inv_freq, sections=None, adjacent: bool = False, cyclic: bool = False, out=None,
          stream=None):
     """Rotary positions: q [..., Hq, d], k and v [..., Hkv, d] bf16 (strided views of a fused projection's
-    output will do; any may be None), positions [n_axes, T] or [T] int32, inv_freq [rotary_dim / 2] fp32,
-    sections: pairs per axis (None: one axis) -> contiguous (q, k, v), or out = (q, k, v) to write to."""
+    output will do; any may be None), positions [n_axes, T] int32 (one axis: [T]; T may be the axes "..."),
+    inv_freq [rotary_dim / 2] fp32, sections: pairs per axis (None: one axis) -> contiguous (q, k, v), or
+    out = (q, k, v) to write to."""
     return (_native or _load_native()).rope(q, k, v, positions, inv_freq, sections, _rope_flags(adjacent, cyclic), out,
                                             stream)
 

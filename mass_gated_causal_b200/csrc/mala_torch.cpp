@@ -136,7 +136,8 @@ Angles angles(const Place& at_, const Tensor& positions, const Tensor& inv_freq,
   a.n_axes = sections ? static_cast<int>(std::min<size_t>(sections->size(), 8)) : 1;
   a.sections[0] = a.rotary_dim / 2;
   for (int i = 0; sections && i < a.n_axes; ++i) a.sections[i] = c_int(at_.where, (*sections)[i]);
-  if (positions.numel() != a.n_axes * T)
+  // (as many values in another layout, a token's axes side by side, say, would be read as other positions)
+  if (positions.numel() != a.n_axes * T || (a.n_axes > 1 && positions.dim() > 1 && positions.size(0) != a.n_axes))
     refuse(at_.where, "positions must be [", a.n_axes, ", ", T, "], got ", positions.sizes());
   return a;
 }
