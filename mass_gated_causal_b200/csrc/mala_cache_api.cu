@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "mala_evict.cuh"
+#include "mala_evict_check.h"
 #include "mala_host.h"
 #include "mala_rope.cuh"
 
@@ -281,21 +282,10 @@ int mala_evict_gather(const void* k_pages, const void* v_pages, const int32_t* b
                       const int32_t* new_seqlens, void* k_out_pages, void* v_out_pages, const int32_t* out_table,
                       int B, int Hkv, int budget, int num_pages, int num_out_pages, int page_size,
                       int max_pages_per_seq, int max_out_pages_per_seq, int d, void* stream) {
-  if (!k_pages || !v_pages || !block_table || !index || !new_seqlens || !k_out_pages || !v_out_pages || !out_table)
-    return MALA_ERR_INVALID_ARG;
-  if (B < 1 || Hkv < 1 || budget < 1 || num_pages < 1 || num_out_pages < 1 || max_pages_per_seq < 1 ||
-      max_out_pages_per_seq < 1)
-    return MALA_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return MALA_ERR_UNSUPPORTED;
-  if (page_size != 64 && page_size != 128) return MALA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_out_pages_per_seq) * page_size < budget) return MALA_ERR_INVALID_ARG;
-  const long long most = std::max(num_pages, num_out_pages);
-  if (static_cast<long long>(max_pages_per_seq) * page_size >= (1ll << 31) || most * page_size >= (1ll << 31) ||
-      most * page_size * Hkv * d >= (1ll << 40) || B > 65535)
-    return MALA_ERR_UNSUPPORTED;
-  const void* ptrs[] = {k_pages, v_pages, k_out_pages, v_out_pages};
-  for (const void* x : ptrs)
-    if (!aligned16(x)) return MALA_ERR_UNSUPPORTED;
+  const int rc = mala::check_gather(k_pages, v_pages, block_table, index, new_seqlens, k_out_pages, v_out_pages,
+                                    out_table, B, Hkv, budget, num_pages, num_out_pages, page_size, max_pages_per_seq,
+                                    max_out_pages_per_seq, d);
+  if (rc != MALA_OK) return rc;
   mala::GatherParams p = {};
   p.k = static_cast<const uint4*>(k_pages);
   p.v = static_cast<const uint4*>(v_pages);

@@ -13,6 +13,7 @@
 #include <sstream>
 
 #include "../../include/mala.h"
+#include "mala_evict_check.h"
 
 namespace py = pybind11;
 using at::Tensor;
@@ -359,31 +360,54 @@ std::tuple<Tensor, Tensor, Tensor> evict_select(const Tensor& mass, const Tensor
   return {index, fresh, out};
 }
 
+// The pools and tables of a copy of [B, Hkv, budget] rows, checked.
+struct Copy {
+  const Tensor &k, &v, &table, &to, &ko, &vo;
+  int B, Hkv, budget, pages, out_pages, page, max_pages, max_out, d;
+
+  Copy(const Place& at_, int64_t B_, int64_t Hkv_, int64_t budget_, const Tensor& k_, const Tensor& v_,
+       const Tensor& table_, const Tensor& to_, const OptTensor& k_out, const OptTensor& v_out)
+      : k(k_), v(v_), table(table_), to(to_), ko(k_out ? *k_out : k_), vo(v_out ? *v_out : v_) {
+    const char* where = at_.where;
+    for (const Tensor* x : {&table, &to}) at_.need(*x, kI32);
+    for (const Tensor* x : {&k, &v, &ko, &vo}) at_.need(*x, kBf16);
+    const auto pool = k.sizes(), out = ko.sizes();
+    if (pool.size() != 4 || out.size() != 4 || pool[2] != Hkv_ || pool.slice(1) != out.slice(1) || v.sizes() != pool ||
+        vo.sizes() != out)
+      refuse(where, "pools must be [num_pages, page, ", Hkv_, ", d], got ", pool, ", ", v.sizes(), ", ", out, " and ",
+             vo.sizes());
+    if (table.dim() != 2 || table.size(0) != B_ || to.dim() != 2 || to.size(0) != B_)
+      refuse(where, "block_table and out_table must be [", B_, ", pages]");
+    B = c_int(where, B_);
+    Hkv = c_int(where, Hkv_);
+    budget = c_int(where, budget_);
+    pages = c_int(where, pool[0]);
+    out_pages = c_int(where, out[0]);
+    page = c_int(where, pool[1]);
+    d = c_int(where, pool[3]);
+    max_pages = c_int(where, table.size(1));
+    max_out = c_int(where, to.size(1));
+  }
+  void run(const Place& at_, const Tensor& index, const Tensor& lens) const {
+    check(mala_evict_gather(k.data_ptr(), v.data_ptr(), iptr(table), iptr(index), iptr(lens), ko.data_ptr(),
+                            vo.data_ptr(), iptr(to), B, Hkv, budget, pages, out_pages, page, max_pages, max_out, d,
+                            at_.handle()),
+          at_.where);
+  }
+};
+
 std::tuple<Tensor, Tensor> evict_gather(const Tensor& index, const Tensor& new_seqlens, const Tensor& k_pages,
                                         const Tensor& v_pages, const Tensor& block_table, const Tensor& out_table,
                                         const OptTensor& k_out, const OptTensor& v_out, const py::object& stream) {
   const char* where = "mala_evict_gather";
   const Place place(where, index, stream);
-  const Tensor &ko = k_out ? *k_out : k_pages, &vo = v_out ? *v_out : v_pages;
-  for (const Tensor* x : {&index, &new_seqlens, &block_table, &out_table}) place.need(*x, kI32);
-  for (const Tensor* x : {&k_pages, &v_pages, &ko, &vo}) place.need(*x, kBf16);
+  for (const Tensor* x : {&index, &new_seqlens}) place.need(*x, kI32);
   if (index.dim() != 3) refuse(where, "index must be [B, Hkv, budget], got ", index.sizes());
-  const int64_t B = index.size(0), Hkv = index.size(1), budget = index.size(2);
-  const auto pool = k_pages.sizes(), to = ko.sizes();
-  if (pool.size() != 4 || to.size() != 4 || pool[2] != Hkv || pool.slice(1) != to.slice(1) || v_pages.sizes() != pool ||
-      vo.sizes() != to)
-    refuse(where, "pools must be [num_pages, page, ", Hkv, ", d], got ", pool, ", ", v_pages.sizes(), ", ", to, " and ",
-           vo.sizes());
-  place.shape(new_seqlens, "new_seqlens", {B});
-  if (block_table.dim() != 2 || block_table.size(0) != B || out_table.dim() != 2 || out_table.size(0) != B)
-    refuse(where, "block_table and out_table must be [", B, ", pages]");
-  check(mala_evict_gather(k_pages.data_ptr(), v_pages.data_ptr(), iptr(block_table), iptr(index), iptr(new_seqlens),
-                          ko.data_ptr(), vo.data_ptr(), iptr(out_table), c_int(where, B), c_int(where, Hkv),
-                          c_int(where, budget), c_int(where, pool[0]), c_int(where, to[0]), c_int(where, pool[1]),
-                          c_int(where, block_table.size(1)), c_int(where, out_table.size(1)), c_int(where, pool[3]),
-                          place.handle()),
-        where);
-  return {ko, vo};
+  place.shape(new_seqlens, "new_seqlens", {index.size(0)});
+  const Copy copy(place, index.size(0), index.size(1), index.size(2), k_pages, v_pages, block_table, out_table, k_out,
+                  v_out);
+  copy.run(place, index, new_seqlens);
+  return {copy.ko, copy.vo};
 }
 
 std::tuple<Tensor, Tensor, Tensor> evict(const Tensor& mass, const Tensor& seqlens_k, int64_t budget,
@@ -391,9 +415,18 @@ std::tuple<Tensor, Tensor, Tensor> evict(const Tensor& mass, const Tensor& seqle
                                          const Tensor& out_table, int64_t n_sink, int64_t n_recent,
                                          const OptTensor& k_out, const OptTensor& v_out, const OptTensor& mass_to,
                                          const py::object& stream) {
+  const char* where = "mala_evict_gather";
+  const Place place(where, mass, stream);
+  if (mass.dim() != 3) refuse(where, "mass must be [B, Hkv, ld], got ", mass.sizes());
+  // what the copy would refuse is refused before the selection writes anything
+  const Copy copy(place, mass.size(0), mass.size(1), budget, k_pages, v_pages, block_table, out_table, k_out, v_out);
+  if (budget >= 1)  // (the selection refuses others; its lists have no pointers yet, so the masses' stand for them)
+    check(mala::check_gather(k_pages.data_ptr(), v_pages.data_ptr(), iptr(block_table), fptr(mass), fptr(mass),
+                             copy.ko.data_ptr(), copy.vo.data_ptr(), iptr(out_table), copy.B, copy.Hkv, copy.budget,
+                             copy.pages, copy.out_pages, copy.page, copy.max_pages, copy.max_out, copy.d),
+          where);
   auto rows_left = evict_select(mass, seqlens_k, budget, n_sink, n_recent, mass_to, stream);
-  evict_gather(std::get<0>(rows_left), std::get<1>(rows_left), k_pages, v_pages, block_table, out_table, k_out, v_out,
-               stream);
+  copy.run(place, std::get<0>(rows_left), std::get<1>(rows_left));
   return rows_left;
 }
 
