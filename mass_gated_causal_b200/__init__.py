@@ -533,9 +533,11 @@ def _load_native():
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing (run `python mass_gated_causal_b200/build.py`)")
     spec = importlib.util.spec_from_file_location("mala_torch", path)
-    _native = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_native)
-    return _native
+    native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(native)
+    native.set_error_class(MalaError)
+    _native = native  # only now, for other threads and after a load that failed
+    return native
 
 
 def _rope_flags(adjacent, cyclic):

@@ -29,9 +29,13 @@ template <typename... A>
   throw py::value_error(s.str());
 }
 
+// The package's MalaError, set when the package loads this module (under whatever name it has
+// itself); never released, as the interpreter may be gone by then.
+PyObject* error_class = nullptr;
+
 void check(int rc, const char* where) {
   if (rc == MALA_OK) return;
-  const py::object cls = py::module_::import("mass_gated_causal_b200").attr("MalaError");
+  const auto cls = py::reinterpret_borrow<py::object>(error_class ? error_class : PyExc_RuntimeError);
   const py::object error = cls(rc, where);
   PyErr_SetObject(cls.ptr(), error.ptr());
   throw py::error_already_set();
@@ -433,6 +437,7 @@ std::tuple<Tensor, Tensor, Tensor> evict(const Tensor& mass, const Tensor& seqle
 }  // namespace
 
 PYBIND11_MODULE(mala_torch, m) {
+  m.def("set_error_class", [](const py::object& cls) { error_class = py::object(cls).release().ptr(); });
   m.def("rows", [](const Tensor& x) {
     const Rows r = rows("rows", x);
     return py::make_tuple(r.tokens, r.heads, r.d, r.tok, r.head);
