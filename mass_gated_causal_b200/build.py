@@ -5,11 +5,13 @@ nvcc cross-compiles for sm_100a without a GPU. Every csrc/*.cu is one
 translation unit, compiled to an object of its own (several at a time, and only
 when one of the files it includes has changed, unless forced) and linked with
 the static CUDA runtime, so the library carries no dependency on a particular
-libcudart. Run as a script (`python mass_gated_causal_b200/build.py`): the
+libcudart. It needs neither torch nor Python; the torch side is left out, with a
+note, where torch is not installed. Run as a script (`python mass_gated_causal_b200/build.py`): the
 package itself refuses to import while the library is missing.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import re
 import subprocess
@@ -54,8 +56,14 @@ def _stale(out, files) -> bool:
     return not os.path.exists(out) or any(os.path.getmtime(f) > os.path.getmtime(out) for f in files)
 
 
+def _has_torch() -> bool:
+    """The C library needs no torch: without it only the torch side is left out."""
+    return importlib.util.find_spec("torch") is not None
+
+
 def needs_build() -> bool:
-    return any(_stale(LIB, _files_of(s)) for s in sources()) or _stale(TORCH_LIB, _files_of(TORCH_SRC))
+    return any(_stale(LIB, _files_of(s)) for s in sources()) or (_has_torch() and
+                                                                 _stale(TORCH_LIB, _files_of(TORCH_SRC)))
 
 
 def _build_torch_side() -> None:
@@ -96,7 +104,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC] + FLAGS + ["-shared", "-Xlinker", "-soname=libmala.so"] + objs + ["-o", tmp])
     os.replace(tmp, LIB)
-    if force or _stale(TORCH_LIB, _files_of(TORCH_SRC)):
+    if not _has_torch():
+        print("torch is not installed: mala_torch.so, the torch side of the calls beside attention, is not built")
+    elif force or _stale(TORCH_LIB, _files_of(TORCH_SRC)):
         _build_torch_side()
     return LIB
 
