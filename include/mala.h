@@ -562,9 +562,9 @@ MALA_API int mala_decode_paged_mass(const void* q, const void* k_pages, const vo
  *              length is reported by mala_check_status and counts as 0)
  *   index      [B, Hkv, budget] int32, out: the remaining rows, ascending; -1
  *              past min(L, budget)
- *   new_seqlens [B] int32, out: min(L, budget) (not the array seqlens_k)
+ *   new_seqlens [B] int32, out: min(L, budget) (it must not overlap seqlens_k)
  *   mass_out   [B, Hkv, ld_mass_out] fp32, out, nullable: the remaining rows'
- *              masses, 0 past them; ld_mass_out >= budget
+ *              masses, 0 past them; ld_mass_out >= budget. Must not overlap mass.
  *   budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget
  */
 MALA_API int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* index, int32_t* new_seqlens,

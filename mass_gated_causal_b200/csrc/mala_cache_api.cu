@@ -95,6 +95,12 @@ int launch_rope(mala::RopeParams p, int d, bool adjacent, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ evict
+// Whether two arrays (their bytes) share any.
+bool overlap(const void* a, long long na, const void* b, long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<unsigned long long>(nb) && y < x + static_cast<unsigned long long>(na);
+}
+
 template <int C, int kKeep>
 int launch_select_keep(const mala::EvictParams& p, cudaStream_t st) {
   auto kern = mala::mala_evict_select_kernel<C, kKeep>;
@@ -243,12 +249,17 @@ int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* inde
   if (!mass || !seqlens_k || !index || !new_seqlens) return MALA_ERR_INVALID_ARG;
   if (B < 1 || Hkv < 1 || ld_mass < 1 || budget < 1 || n_sink < 0 || n_recent < 0) return MALA_ERR_INVALID_ARG;
   if (static_cast<long long>(n_sink) + n_recent > budget) return MALA_ERR_INVALID_ARG;
-  if (new_seqlens == seqlens_k) return MALA_ERR_INVALID_ARG;  // other blocks still read the old lengths
-  if (mass_out && (ld_mass_out < budget || mass_out == mass)) return MALA_ERR_INVALID_ARG;
+  if (new_seqlens == seqlens_k || mass_out == mass) return MALA_ERR_INVALID_ARG;
+  if (mass_out && ld_mass_out < budget) return MALA_ERR_INVALID_ARG;
   if (!aligned16(mass) || !aligned16(index) || (mass_out && !aligned16(mass_out))) return MALA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hkv >= (1ll << 24) || ld_mass > (1 << 30) || budget > (1 << 30) ||
       (mass_out && ld_mass_out > (1 << 30)))
     return MALA_ERR_UNSUPPORTED;
+  // what one block writes, another may still read
+  const long long rows = static_cast<long long>(B) * Hkv;
+  if (overlap(new_seqlens, 4ll * B, seqlens_k, 4ll * B) ||
+      (mass_out && overlap(mass_out, 4 * rows * ld_mass_out, mass, 4 * rows * ld_mass)))
+    return MALA_ERR_INVALID_ARG;
   mala::EvictParams p = {};
   p.mass = mass;
   p.seqlens = seqlens_k;
@@ -267,7 +278,6 @@ int mala_evict_select(const float* mass, const int32_t* seqlens_k, int32_t* inde
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // CTAs per row of masses: as many as keep all rows on the GPU at once (one
   // CTA to an SM), but no more than leave each 2K masses
-  const long long rows = static_cast<long long>(B) * Hkv;
   int cluster = 1;
   while (cluster < 8 && rows * cluster * 2 <= sm_count() && ld_mass > 2048 * cluster) cluster *= 2;
   switch (cluster) {

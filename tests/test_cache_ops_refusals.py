@@ -1,0 +1,17 @@
+"""More of what the host refuses of the operators beside attention (no call here reaches CUDA)."""
+import pytest
+
+from test_cache_ops_abi import P, select
+
+
+@pytest.mark.parametrize("kw", [
+    # 2 x 2 rows of 1000 masses from P on: the last byte of them, the first row's end, all of them within
+    dict(mass_out=P + 4 * 4000 - 16), dict(mass_out=P + 4 * 1000), dict(mass=1 << 20, mass_out=(1 << 20) - 16),
+    dict(mass=1 << 20, mass_out=(1 << 20) - 4 * 4 * 200 + 16),  # 2 x 2 x 200 masses out, their last four
+    dict(mass=1 << 20, mass_out=1 << 24, new_seqlens=4 * P, seqlens_k=4 * P + 4),
+    dict(mass=1 << 20, mass_out=1 << 24, new_seqlens=4 * P + 4, seqlens_k=4 * P),
+])
+def test_evict_select_rejects_overlaps(kw):
+    a = dict(mass=P, mass_out=1 << 24, index=1 << 22, new_seqlens=1 << 23, seqlens_k=(1 << 23) + 8)
+    a.update(kw)
+    assert select(**a) == 1
