@@ -158,7 +158,7 @@ extern "C" {
 
 size_t mala_decode_mass_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages_per_seq,
                                        int n_splits) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || max_pages_per_seq < 1 || n_splits < 0 || (d != 64 && d != 128) ||
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_pages_per_seq < 1 || n_splits < 0 || (d != 64 && d != 128) ||
       (page_size != 64 && page_size != 128))
     return 0;
   return layout(B, Hq, Hkv, static_cast<long long>(max_pages_per_seq) * page_size, d, n_splits).total;

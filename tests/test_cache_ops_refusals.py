@@ -1,6 +1,7 @@
 """More of what the host refuses of the operators beside attention (no call here reaches CUDA)."""
 import pytest
 
+import mass_gated_causal_b200 as mala
 from test_cache_ops_abi import P, select
 
 
@@ -15,3 +16,9 @@ def test_evict_select_rejects_overlaps(kw):
     a = dict(mass=P, mass_out=1 << 24, index=1 << 22, new_seqlens=1 << 23, seqlens_k=(1 << 23) + 8)
     a.update(kw)
     assert select(**a) == 1
+
+
+def test_workspace_of_heads_that_do_not_group_is_0():
+    assert mala.mala_decode_mass_workspace_size(4, 8, 2, 128, 128, 40, 0) > 0
+    assert mala.mala_decode_mass_workspace_size(4, 8, 3, 128, 128, 40, 0) == 0
+    assert mala.mala_decode_mass_workspace_size(4, 2, 8, 128, 128, 40, 4) == 0
