@@ -135,7 +135,8 @@ int launch_select(const mala::EvictParams& p, cudaStream_t st) {
   const int each = (p.ld + C * mala::kEvictThreads - 1) / (C * mala::kEvictThreads);
   // (keys kept for 1, 4, 16 or 32 of them: 1K rows of masses 3.7 us with one, 4.0 with room for four;
   // 64 rows of 64K masses 18.4 us with 32, 48 with every pass reading the masses again)
-  if (each <= 1) return launch_select_keep<C, 1>(p, st);
+  if constexpr (C == 1)  // (a cluster's threads meet two at least: it is chosen for more than 1024 C masses)
+    if (each <= 1) return launch_select_keep<C, 1>(p, st);
   if (each <= 4) return launch_select_keep<C, 4>(p, st);
   if (each <= 16) return launch_select_keep<C, 16>(p, st);
   if (each <= 32) return launch_select_keep<C, 32>(p, st);

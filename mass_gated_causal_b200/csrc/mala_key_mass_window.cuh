@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
   constexpr uint32_t IDESC = idesc_bf16(128, kCols, false, false);
   constexpr int STEP = Lay::STEP;
   constexpr int CG = kCols / 2;  // columns per compute warp
+  static_assert(CG % 32 == 0, "a warp reads its columns 32 at a time");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sLse = reinterpret_cast<float*>(smem + Lay::OFF_LSE);
@@ -257,18 +258,16 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
       for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
 #pragma unroll
       for (int c0 = 0; c0 < CG; c0 += 32) {
-        constexpr int kLast = (CG - 1) / 32 * 32;
         uint32_t sv[32];
-        if (CG - c0 >= 32) tmem_ld32(tS + c0, sv);
-        else tmem_ld16(tS + c0, *reinterpret_cast<uint32_t(*)[16]>(sv));
+        tmem_ld32(tS + c0, sv);
         tmem_ld_wait();
-        if (c0 == kLast) {  // the block is out of TMEM: its columns go back to the MMA issuer
+        if (c0 == CG - 32) {  // the block is out of TMEM: its columns go back to the MMA issuer
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[team]);
         }
 #pragma unroll
-        for (int j = 0; j < 32 && c0 + j < CG; j += 16) {
+        for (int j = 0; j < 32; j += 16) {
           uint64_t v[8];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (c0 + j + 2 * e) * 4, v[e], v[e + 1]);
