@@ -15,13 +15,24 @@
 // operand of every MMA; only Q passes through shared memory, which halves the
 // operand traffic of an MMA whose both operands lie there (at N = 128 that
 // traffic is as long as the MMA itself).
+// The LSEs go through the tensor cores too: -LSE / scale in four bf16 parts (exact to
+// 2^-33) are four more channels of a row of Q, against ones on the keys' side, so that
+// what comes out is s - LSE and a thread only scales it. That is for the bits that the
+// accumulator drops (toward zero, about half a step of every partial sum but the last):
+// taken off at the end, the partial sums run up to s and every weight is too small, by
+// 1.2e-6 on average over an 8K prompt and 1.9e-6 with scores of 40; taken off in the
+// first place, they run from -LSE and it is too large. After five eighths of the
+// channels (lse_step) the sums before and after partly cancel, for concentrated rows
+// (s near LSE) and diffuse ones (s small against it): 1.8e-7 to 6.9e-7 in relative L2
+// for prompts, random keys and large scores, and sums without dropped bits stay exact.
+// It also spares a thread the loads of the LSEs, which pays for the step.
 //   warps 0-15  compute: warps 8 x .. 8 x + 7 work on tile x, four on the first 64
 //               queries of a query tile and four on the others; a thread reads its
 //               key's 64 scores out of TMEM, hands the columns back, and sums the
 //               exponentials
-//   warp  16    producer: Q tiles by TMA and the rows' -LSE log2(e), a ring
+//   warp  16    producer: Q tiles by TMA and the rows' LSEs, a ring
 //   warp  17    MMA issuer (one thread), the tiles in turn
-// TMEM: S (2 x 128 columns) | K (2 x D / 2 columns).
+// TMEM: S (2 x 128 columns) | K (2 x D / 2 columns) | ones (8 columns).
 //
 // Bound: with d = 128 a 128 x 128 tile takes 512 cycles of MMA and 16,384
 // exponentials, 1,024 cycles at the special-function unit's 16 a cycle; one of
@@ -56,7 +67,7 @@ struct KeyMassParams {
   const int* cu_k;
   int total_q, total_k;
   float scale_log2, decay;
-  float lse_hi, lse_lo;  // log2(e) as the rounded scale_log2 has it, in two parts (neg_lse2)
+  float inv_hi, inv_lo;  // 1 / scale, in two parts (lse_operand)
   const float* mass_in;  // [B, Hkv, ld], nullable
   float* mass_out;
   int ld;
@@ -78,8 +89,9 @@ struct KeyMassLayout {
   static constexpr int THREADS = (CW + 2) * 32;
   static constexpr int Q_BYTES = 128 * D * 2;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_LSE = OFF_Q + NQ * Q_BYTES;  // fp32 [NQ][128]
-  static constexpr int OFF_RED = OFF_LSE + NQ * 512;    // fp32 [NT][128]: the second half's sums
+  static constexpr int LSE_BYTES = 128 * 32;  // [NQ][128 rows][16 bf16]: the LSEs' channels (lse_offset)
+  static constexpr int OFF_LSE = OFF_Q + NQ * Q_BYTES;
+  static constexpr int OFF_RED = OFF_LSE + NQ * LSE_BYTES;  // fp32 [NT][128]: the second half's sums
   static constexpr int OFF_BAR = OFF_RED + NT * 512;
   // q_full[NQ], q_empty[NQ], s_full[NT], s_empty[NT], k_ready, mma_final
   static constexpr int N_BARS = 2 * NQ + 2 * NT + 2;
@@ -88,7 +100,7 @@ struct KeyMassLayout {
   // at least half of an SM's shared memory: a second CTA on the SM would wait for tensor memory
   static constexpr int LEAST = 118 * 1024;
   static constexpr int ALLOC_BYTES = (BYTES > LEAST ? BYTES : LEAST) + 1024;
-  static constexpr int COL_S = 0, COL_K = NT * 128;
+  static constexpr int COL_S = 0, COL_K = NT * 128, COL_ONE = COL_K + NT * (D / 2);
   static constexpr int TMEM_COLS = 512;
   static_assert(ALLOC_BYTES <= 232448, "shared memory exceeds the per-CTA limit");
 };
@@ -122,12 +134,26 @@ __device__ __forceinline__ int key_mass_qt0(const KeyMassSeq& s, int k0) {
   return max(0, k0 - s.P0 - s.first) / 128;
 }
 
-// -LSE in the units of the scores: times the log2(e) that the rounded scale_log2
-// applies to them, not one rounded on its own (the difference, up to 6e-8 of a
-// score of 20, would be an error of every weight).
-__device__ __forceinline__ float neg_lse2(const KeyMassParams& p, float lse) {
-  return fabsf(lse) == INFINITY ? -lse : -fmaf(lse, p.lse_hi, lse * p.lse_lo);
+// -LSE in the units of the products q k, as four bf16 values whose sum is exact to 2^-33:
+// the four channels that the MMA issuer adds to a row of Q.
+__device__ __forceinline__ uint2 lse_operand(const KeyMassParams& p, float lse) {
+  const float a = lse * p.inv_hi;
+  const bool fin = fabsf(a) < INFINITY;
+  const float e = fin ? fmaf(lse, p.inv_hi, -a) + lse * p.inv_lo : 0.f;
+  const float hi = bf16lo_to_f32(pack_bf16x2(-a, 0.f));
+  const float r = fin ? -a - hi : 0.f;  // (an infinity or NaN stands alone)
+  const uint32_t w0 = pack_bf16x2(hi, r);
+  return make_uint2(w0, pack_bf16x2(r - bf16hi_to_f32(w0), -e));
 }
+
+// Where chunk `chunk` (of two) of row `row` of that operand lies: 8-row blocks of each chunk.
+__device__ __forceinline__ uint32_t lse_offset(int row, int chunk) {
+  return (row >> 3) * 256 + chunk * 128 + (row & 7) * 16;
+}
+__device__ __forceinline__ uint64_t lse_desc(uint32_t saddr) { return sdesc_plain(saddr, 128, 256); }
+
+// After how many of the D / 16 steps over the channels the LSEs' step comes (see above).
+constexpr int lse_step(int d) { return (5 * (d / 16) + 7) / 8; }
 
 // 2^x of a packed pair on the FMA pipes: x = n + f with n the nearest integer,
 // |f| <= 1/2; 2^f by a polynomial of degree 5 (minimax in the relative error, by
@@ -166,7 +192,7 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + Lay::OFF_Q;
-  float* sLse = reinterpret_cast<float*>(smem + Lay::OFF_LSE);
+  const uint32_t sLse = smem_u32(smem + Lay::OFF_LSE);
   float* sRed = reinterpret_cast<float*>(smem + Lay::OFF_RED);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
   uint64_t* q_empty = q_full + NQ;
@@ -233,7 +259,7 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NQ; ++i) {
       mbar_init(&q_full[i], 2);
-      mbar_init(&q_empty[i], 1 + CW);
+      mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < NT; ++i) {
       mbar_init(&s_full[i], 1);
@@ -249,6 +275,9 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
     tmem_relinquish();
     if (lane == 0) prefetch_tensormap(&tm_q);
   }
+  for (int i = threadIdx.x; i < NQ * Lay::LSE_BYTES / 16; i += Lay::THREADS)  // channels 4 .. 15 stay 0
+    st_shared_v4(sLse + i * 16, 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -285,7 +314,11 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
       }
       issued = n + 1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sLse[st * 128 + e * 32 + lane] = neg_lse2(p, cur[e]);
+      for (int e = 0; e < 4; ++e) {
+        const uint2 w = lse_operand(p, cur[e]);
+        st_shared_v2(sLse + st * Lay::LSE_BYTES + lse_offset(e * 32 + lane, 0), w.x, w.y);
+      }
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[st]);
 #pragma unroll
@@ -303,7 +336,7 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
   } else if (warp == CW + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dLse = lse_desc(sLse);
       bool ok = mbar_wait(k_ready, 0, fs);
       tc_fence_after();
       for (int n = 0; ok && n < N; ++n) {
@@ -319,10 +352,14 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
           }
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
+          for (int kk = 0; kk < D / 16; ++kk) {
             umma_f16_ts(tmem + Lay::COL_S + y * 128, tmem + Lay::COL_K + y * (D / 2) + kk * 8,
                         sdesc_add(dQ, st * Lay::Q_BYTES + (kk >> 2) * 16384 + (kk & 3) * 32), IDESC,
                         kk > 0 ? 1u : 0u);
+            if (kk + 1 == lse_step(D))
+              umma_f16_ts(tmem + Lay::COL_S + y * 128, tmem + Lay::COL_ONE, sdesc_add(dLse, st * Lay::LSE_BYTES),
+                          IDESC, 1u);
+          }
           umma_commit(&s_full[y]);
         }
         if (ok) umma_commit(&q_empty[st]);
@@ -338,6 +375,10 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
       __syncwarp();
       if constexpr (W == 32) tmem_st32(tK, w);
       else tmem_st16(tK, *reinterpret_cast<uint32_t(*)[16]>(w));
+      if (x == 0 && half == 0) {  // channels 0 .. 3 of the LSEs' step: 1 for every key
+        uint32_t one[16] = {0x3f803f80u, 0x3f803f80u};
+        tmem_st16(tmem + Lay::COL_ONE + lane_base, one);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -346,12 +387,11 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
     const uint32_t tS = tmem + Lay::COL_S + x * 128 + half * 64 + lane_base;
     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
     const int kw0 = k0 + x * 128 + wq * 32;  // the warp's first key
-    const uint32_t lse_s = smem_u32(sLse) + half * 256;
     float sum = 0.f, comp = 0.f;  // compensated over the tiles: a key may be seen by 10^5 queries
     bool aborted = false;
     // one 64 x 1 strip of an item: the sum of this key's weights over the strip's queries.
     // kPlain: every row of the strip counts and sees every key of the warp.
-    auto strip = [&](auto plain_c, uint32_t la, int c_lo, int c_hi) -> float {
+    auto strip = [&](auto plain_c, int c_lo, int c_hi) -> float {
       constexpr bool kPlain = decltype(plain_c)::value;
       uint64_t acc[4];
 #pragma unroll
@@ -370,10 +410,8 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
         for (int j = 0; j < 32; j += 16) {
           uint64_t v[8];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (c0 + j + 2 * e) * 4, v[e], v[e + 1]);
-#pragma unroll
           for (int e = 0; e < 8; ++e)
-            v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
+            v[e] = f2_mul(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (kPlain && e % 2 == 1 && e < 2 * kMassPoly) {
@@ -398,43 +436,30 @@ __global__ void __launch_bounds__(KeyMassLayout<D>::THREADS, 1)
       f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
       return lo + hi;
     };
-    int st = 0, g = 0;
-    uint32_t q_par = 0, s_par = 0;
+    int g = 0;
+    uint32_t s_par = 0;
     int r0 = sq.first + qt_a * 128 + half * 64;  // this warp's first row of the item
     for (int n = 0; n < N; ++n) {
       if (!mbar_wait_warp(&s_full[x], s_par, fs)) {
         aborted = true;
         break;
       }
-      // the tile's LSEs: written before this phase of q_full completed, which the
-      // MMA thread waited for before the scores; the wait makes them visible here
-      if (!mbar_wait_warp(&q_full[st], q_par, fs)) {
-        aborted = true;
-        break;
-      }
       tc_fence_after();
       const int pos0 = sq.P0 + r0;  // position of the first row
-      const uint32_t la = lse_s + st * 512;
       float tile = 0.f;
       if (kw0 + 31 <= pos0 && r0 + 64 <= sq.Lq) {
-        tile = strip(std::true_type(), la, 0, 0);
+        tile = strip(std::true_type(), 0, 0);
       } else if (kw0 <= pos0 + 63 && r0 < sq.Lq && kw0 < sq.Lk) {
-        tile = strip(std::false_type(), la, key - pos0, sq.Lq - r0);
+        tile = strip(std::false_type(), key - pos0, sq.Lq - r0);
       } else {  // no row sees a key of the warp
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[x]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_empty[st]);  // this warp has read the LSEs
       const float y = tile - comp, t = sum + y;
       comp = (t - sum) - y;
       sum = t;
       s_par ^= 1u;
-      if (++st == NQ) {
-        st = 0;
-        q_par ^= 1u;
-      }
       if (++g == p.G) {
         g = 0;
         r0 += 128;

@@ -149,16 +149,10 @@ int run(const void* q, const void* k, const float* lse, const float* mass_in, fl
   p.cu_k = cu_k;
   p.total_q = total_q;
   p.total_k = total_k;
-  // log2(e) as the rounded scale_log2 has it, for the LSE (neg_lse2). The scores stay as the
-  // tensor core sums them, which drops bits: a score comes out up to half a step too small
-  // for each partial sum of its d / 16 (nothing where the partial sums are exact). mala_fwd's
-  // scores lose the same, so beside its LSE nothing is to be taken back: the weights of a row
-  // of 1,500 random keys (d = 128) sum to 1 - 1e-8, and each is within 8e-8 of the softmax;
-  // against an LSE from elsewhere they are 3e-7 too small on average there.
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  const double ratio = p.scale_log2 / static_cast<double>(scale);
-  p.lse_hi = static_cast<float>(ratio);
-  p.lse_lo = static_cast<float>(ratio - p.lse_hi);
+  const double inv = 1.0 / static_cast<double>(scale);
+  p.inv_hi = static_cast<float>(inv);
+  p.inv_lo = static_cast<float>(inv - p.inv_hi);
   p.decay = decay;
   p.mass_in = mass_in;
   p.mass_out = mass_out;

@@ -46,9 +46,8 @@ struct WinLayout {
   static constexpr int MAX_STAGES = 4;
   static constexpr int STEP = kBlocks == 1 ? 2 : 1;  // between a team's tiles
   static constexpr int AHEAD = 6 / STEP;  // a team's tiles that the earlier masses are fetched ahead (a tile may take 0.3 us)
-  // lse [512], pos [512], sums [2][4][128], earlier masses [STEP][AHEAD + 1][128], then barriers
-  static constexpr int OFF_LSE = 0;
-  static constexpr int OFF_POS = OFF_LSE + kWinMaxCols * 4;
+  // pos [512], sums [2][4][128], earlier masses [STEP][AHEAD + 1][128], then barriers
+  static constexpr int OFF_POS = 0;
   static constexpr int OFF_RED = OFF_POS + kWinMaxCols * 4;
   static constexpr int OFF_OLD = OFF_RED + 2 * 4 * 128 * 4;
   static constexpr int OFF_BAR = OFF_OLD + STEP * (AHEAD + 1) * 128 * 4;
@@ -56,7 +55,12 @@ struct WinLayout {
   static constexpr int N_BARS = 2 * MAX_STAGES + 4 + 3;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int OFF_Q = (OFF_MISC + 16 + 1023) & ~1023;
-  static constexpr int bytes(int stages) { return OFF_Q + kBlocks * kCols * D * 2 + stages * K_BYTES + 1024; }
+  // behind Q the LSEs' channels of its columns and those of the keys (16 each, lse_offset), then the K ring
+  static constexpr int OFF_LSE = OFF_Q + kBlocks * kCols * D * 2;
+  static constexpr int OFF_ONE = OFF_LSE + kBlocks * kCols * 32;
+  static constexpr int OFF_K = OFF_ONE + 128 * 32;
+  static_assert(OFF_K % 1024 == 0, "swizzled tiles");
+  static constexpr int bytes(int stages) { return OFF_K + stages * K_BYTES + 1024; }
 };
 
 template <int D, int kCols, int kBlocks>
@@ -71,7 +75,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
   static_assert(CG % 32 == 0, "a warp reads its columns 32 at a time");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* sLse = reinterpret_cast<float*>(smem + Lay::OFF_LSE);
+  const uint32_t sLse = smem_u32(smem + Lay::OFF_LSE), sOne = smem_u32(smem + Lay::OFF_ONE);
   int* sPos = reinterpret_cast<int*>(smem + Lay::OFF_POS);
   float* sRed = reinterpret_cast<float*>(smem + Lay::OFF_RED);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
@@ -85,7 +89,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint8_t* sQ = smem + Lay::OFF_Q;
   constexpr int cols = kBlocks * kCols;  // columns in all
-  uint8_t* sK = sQ + cols * D * 2;
+  uint8_t* sK = smem + Lay::OFF_K;
   const int NK = wp.k_stages;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,18 +139,6 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
       prefetch_tensormap(&tm_k);
     }
   }
-  for (int c = threadIdx.x; c < cols; c += Lay::THREADS) {
-    const int g = c / wp.rows_pad, r = c % wp.rows_pad;
-    const int i = sq.first + r;
-    float l = -INFINITY;
-    if (g < p.G && r < rows) {
-      const int hq = hkv * p.G + g;
-      l = neg_lse2(p, __ldg(p.cu_q != nullptr ? p.lse + static_cast<size_t>(hq) * p.total_q + sq.q_off + i
-                                              : p.lse + (static_cast<size_t>(b) * p.Hq + hq) * sq.Lq + i));
-    }
-    sLse[c] = l;
-    sPos[c] = sq.P0 + i;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -184,6 +176,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dLse = lse_desc(sLse), dOne = lse_desc(sOne);
       bool ok = mbar_wait(q_ready, 0, fs);
       int st = 0, n = 0;
       uint32_t par = 0;
@@ -199,10 +192,13 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
           }
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
+          for (int kk = 0; kk < D / 16; ++kk) {
             umma_bf16_ss(tmem + (n & 1) * 256, sdesc_add(dK, st * Lay::K_BYTES + (kk >> 2) * 16384 + (kk & 3) * 32),
                          sdesc_add(dQ, (kk >> 2) * (cols * 128) + y * (kCols * 128) + (kk & 3) * 32), IDESC,
                          kk > 0 ? 1u : 0u);
+            if (kk + 1 == lse_step(D))
+              umma_bf16_ss(tmem + (n & 1) * 256, dOne, sdesc_add(dLse, y * (kCols * 32)), IDESC, 1u);
+          }
           umma_commit(&s_full[n & 1]);
         }
         if (ok) umma_commit(&k_empty[st]);
@@ -219,6 +215,23 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
     const int wq = warp & 3, cg = (warp >> 2) & 1, team = warp >> 3;
     const int y = kBlocks == 1 ? 0 : team;  // this warp's block
     const int tid = wq * 32 + lane;  // key within the tile
+    // the columns' LSEs and positions, and 1 in the LSEs' channels for every key, while Q and K are on their way
+    for (int c = threadIdx.x; c < cols; c += 16 * 32) {
+      const int g = c / wp.rows_pad, r = c % wp.rows_pad, i = sq.first + r;
+      uint2 w = make_uint2(0xff80u, 0u);  // -infinity: a column of no row
+      if (g < p.G && r < rows) {
+        const int hq = hkv * p.G + g;
+        w = lse_operand(p, __ldg(p.cu_q != nullptr ? p.lse + static_cast<size_t>(hq) * p.total_q + sq.q_off + i
+                                                   : p.lse + (static_cast<size_t>(b) * p.Hq + hq) * sq.Lq + i));
+      }
+      st_shared_v4(sLse + lse_offset(c, 0), w.x, w.y, 0u, 0u);
+      st_shared_v4(sLse + lse_offset(c, 1), 0u, 0u, 0u, 0u);
+      sPos[c] = sq.P0 + i;
+    }
+    if (threadIdx.x < 128) {
+      st_shared_v4(sOne + lse_offset(threadIdx.x, 0), 0x3f803f80u, 0x3f803f80u, 0u, 0u);
+      st_shared_v4(sOne + lse_offset(threadIdx.x, 1), 0u, 0u, 0u, 0u);
+    }
     bool aborted = !mbar_wait_warp(q_full, 0, fs);
     // rows that do not count: of a head past its rows (another sequence's, perhaps), and past the last head
     for (int i = warp * 32 + lane; i < cols * (D / 8); i += 16 * 32) {
@@ -229,11 +242,11 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_ready);
+    if (!aborted) aborted = !mbar_wait_warp(q_ready, 0, fs);  // every warp's positions are in place
 
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
     const uint32_t tS = tmem + team * 256 + cg * CG + lane_base;  // each team has its own buffer of scores
-    const uint32_t la = smem_u32(sLse) + (y * kCols + cg * CG) * 4;
     const int* pos_a = sPos + y * kCols + cg * CG;
     const int p_min = sq.P0 + sq.first;  // position of the first row that counts
     // The warps of the first columns add the earlier masses: each thread copies its key's into its own
@@ -256,7 +269,7 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
       uint64_t acc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = 0ull;  // (+0, +0)
-#pragma unroll
+#pragma unroll 2  // (all four at once spill)
       for (int c0 = 0; c0 < CG; c0 += 32) {
         uint32_t sv[32];
         tmem_ld32(tS + c0, sv);
@@ -270,10 +283,8 @@ __global__ void __launch_bounds__(WinLayout<D, kCols, kBlocks>::THREADS, 1)
         for (int j = 0; j < 32; j += 16) {
           uint64_t v[8];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) ld_shared_2f2(la + (c0 + j + 2 * e) * 4, v[e], v[e + 1]);
-#pragma unroll
           for (int e = 0; e < 8; ++e)
-            v[e] = f2_fma(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2, v[e]);
+            v[e] = f2_mul(f2_pack(__uint_as_float(sv[j + 2 * e]), __uint_as_float(sv[j + 2 * e + 1])), sl2);
           const int* pos = pos_a + c0 + j;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
