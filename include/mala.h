@@ -491,8 +491,9 @@ MALA_API size_t mala_key_mass_varlen_workspace_size(int num_seqs, int Hq, int Hk
  *   mass_in    [B, Hkv, ld_mass] fp32, in, nullable (0); not read if decay == 0
  *   mass_out   [B, Hkv, ld_mass] fp32, out; entries j >= Lk become 0. May be
  *              mass_in.
- *   Lk <= ld_mass <= 2^30, decay >= 0, window >= 0; workspace 256-byte aligned, >=
- *   mala_key_mass_workspace_size(...) bytes (NULL if that is 0)
+ *   2^-64 <= scale <= 2^64, Lk <= ld_mass <= 2^30, decay >= 0, window >= 0;
+ *   workspace 256-byte aligned, >= mala_key_mass_workspace_size(...) bytes (NULL
+ *   if that is 0)
  */
 MALA_API int mala_key_mass(const void* q, const void* k, const float* lse, const float* mass_in, float* mass_out,
              int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale, int window, float decay, int ld_mass,

@@ -116,6 +116,8 @@ int check(int B, int Hq, int Hkv, int Lq, int Lk, int d, float scale, int window
   if (!(scale > 0.f) || !std::isfinite(scale) || !(decay >= 0.f) || !std::isfinite(decay)) return MALA_ERR_INVALID_ARG;
   if (window < 0 || ld < Lk) return MALA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return MALA_ERR_UNSUPPORTED;
+  // (LSE / scale and its bf16 parts stay within fp32's range; so does every score)
+  if (scale < 0x1p-64f || scale > 0x1p64f) return MALA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hkv >= (1ll << 16) || ld > (1 << 30)) return MALA_ERR_UNSUPPORTED;
   return MALA_OK;
 }

@@ -2,7 +2,7 @@
 import pytest
 
 import mass_gated_causal_b200 as mala
-from test_cache_ops_abi import P, select
+from test_cache_ops_abi import P, mass, select, vmass
 
 
 @pytest.mark.parametrize("kw", [
@@ -22,3 +22,9 @@ def test_workspace_of_heads_that_do_not_group_is_0():
     assert mala.mala_decode_mass_workspace_size(4, 8, 2, 128, 128, 40, 0) > 0
     assert mala.mala_decode_mass_workspace_size(4, 8, 3, 128, 128, 40, 0) == 0
     assert mala.mala_decode_mass_workspace_size(4, 2, 8, 128, 128, 40, 4) == 0
+
+
+@pytest.mark.parametrize("scale,code", [(2.0 ** -65, 2), (1e-42, 2), (2.0 ** 65, 2)])
+def test_key_mass_rejects_scales_that_leave_the_range(scale, code):
+    assert mass(scale=scale) == code and vmass(scale=scale) == code
+    assert mass(scale=2.0 ** -64, workspace=None) == 3 and vmass(scale=2.0 ** 64, workspace=None) == 3
