@@ -1,8 +1,8 @@
 // mala_api.cu -- the C ABI declared in include/mala.h.
 //
 // Host side only: argument validation, TMA tensor-map construction, launch
-// configuration (what the library's translation units share is in mala_host.h). Every step of the computation runs in the kernels included
-// below. The driver's cuTensorMapEncodeTiled is reached through
+// configuration (what the library's translation units share is in mala_host.h).
+// Every step of the computation runs in the kernels included below. The driver's cuTensorMapEncodeTiled is reached through
 // cudaGetDriverEntryPoint, so the library loads on machines without a GPU
 // driver (its symbols can be inspected there) and needs no -lcuda.
 #include <cuda.h>

@@ -34,14 +34,14 @@
 //   warp  17    MMA issuer (one thread), the tiles in turn
 // TMEM: S (2 x 128 columns) | K (2 x D / 2 columns) | ones (8 columns).
 //
-// Bound: with d = 128 a 128 x 128 tile takes 512 cycles of MMA and 16,384
-// exponentials, 1,024 cycles at the special-function unit's 16 a cycle; one of
-// every eight pairs goes through packed FMAs instead (exp2_poly2). At 32K keys,
-// 32 heads over 8 KV heads, 4.5 ms (a tile every 1,240 cycles; the MMAs alone would
-// take 2.7 ms at the measured burst rate, the special-function unit 3.3 ms); the
-// GPU runs at its power limit by then (1,000 W at 1.8 GHz), so that more pairs on
-// the FMA pipes are slower although they relieve the unit (none 4.71 ms, one 4.51,
-// two 4.60, three 4.93).
+// Bound: with d = 128 a 128 x 128 tile takes 576 cycles of MMA (64 of them for the
+// LSEs) and 16,384 exponentials, 1,024 cycles at the special-function unit's 16 a
+// cycle; one of every eight pairs goes through packed FMAs instead (exp2_poly2). At
+// 32K keys, 32 heads over 8 KV heads, 4.5 to 4.6 ms (repeats on the same inputs; 4.7
+// with inputs that change), where the products alone would take 2.7 ms at the measured
+// burst rate and the special-function unit 3.3 ms; the GPU runs at its power limit by
+// then (1,000 W at 1.8 GHz), so that more pairs on the FMA pipes are slower although
+// they relieve the unit (none 4.69 ms, one 4.53, two 4.80, three 5.02).
 //
 // Splits: when the key tiles alone do not fill the GPU, each CTA takes
 // chunk_q query tiles and writes partial sums; mala_key_mass_join_kernel adds

@@ -31,9 +31,10 @@ struct Plan {
 // 0.6 of an SM's share of all walks, the walks are whole: they start longest
 // first and the shorter ones even the SMs out. Above that, an SM that got the
 // longest walk would still run when the others are done, so the walks are cut
-// into chunks of half a share: 8K keys, 8 heads over 2 KV heads, 95 us against 289
+// into chunks of half a share: 8K keys, 8 heads over 2 KV heads, 93 us against 288
 // with whole walks. Chunks of a quarter share cost more in starts than they even
-// out (108 us there, and 8K keys of 16 heads 175 us against 155 whole).
+// out (105 us there; 8K keys of 16 heads, which the rule leaves whole, 152 us, 165 in
+// halves of a share and 174 in quarters).
 Plan plan(double units, long long slots, int G, int Lq, int Lk, int window) {
   Plan w = {};
   if (window_cols(G, Lq, window) > 0) return w;  // Q fits in shared memory: the keys stream past it

@@ -13,16 +13,17 @@
 //               columns (one block) they take the tiles in turn, else a block each of
 //               every tile. A warp has 32 keys and half of the block's columns; the
 //               parts' sums meet in shared memory, and the first part's warps write
-//               the result
+//               the result. At the start they lay out the LSEs, while Q and K are on their way
 //   warp  16    producer: Q once, K tiles through a ring
 //   warp  17    MMA issuer (one thread): S^T = K Q^T, two TMEM buffers in turn
 // Columns past a head's rows hold zeros in Q and -infinity in place of -LSE, so
 // they add nothing. Bound: G x W exponentials per key on the
 // special-function unit (at 256 columns 2,048 cycles a tile against 760 for reading
 // K at the HBM rate), a quarter of them moved to the FMA pipes (exp2_poly2). 64 rows
-// of 32 heads over 8 KV heads against 2 x 32,000 keys: 45 us (47 with an eighth on the
-// FMA pipes, 46 with three eighths; 51.5 with all sixteen warps on one tile); one row,
-// which only reads K, 28 us, of which 21 are K's bytes.
+// of 32 heads over 8 KV heads against 2 x 32,000 keys: 41 us over two sets of inputs in
+// turn (43 with an eighth on the FMA pipes, 44.7 with three eighths; all sixteen warps on
+// one tile took 15% longer), 49 where every pass has inputs that no cache holds; one row,
+// which only reads K, 27.5 us, of which 21 are K's bytes.
 #pragma once
 
 #include "mala_key_mass.cuh"
